@@ -308,6 +308,104 @@ ISPA_API ispa_status ispa_tempcache_merge(int32_t n_heads, int32_t head_dim, voi
                                           const int32_t* idx, const float* sim, float threshold, void* stream);
 
 /*
+ * A history held at a fixed budget by accumulated attention weight, for a cache that ISPA's F-Layers
+ * keep growing and TempCache does not merge enough of (not a step of the pages' methods; Future
+ * Forcing's page names the historical attention score as one half of its eviction score).
+ *
+ * ispa_attn_mass: the attention weight that each key of one segment collects from the chunk's queries,
+ *   mass_out[h, j] = decay * mass[h, j] + sum_i exp(softmax_scale q_i.k_j + kv_bias[h, j] - L[h, i]),
+ *   L[h, i] = log(exp(lse_loc[h, i]) + exp(lse_hist[h, i])),
+ * with lse_loc and lse_hist exactly as ispa_dual_stream_attn wrote them for the same queries (fp32
+ * [n_heads, n_q], dense; lse_hist NULL = no history branch).  A row with L = -inf adds nothing.
+ *   q: dtype [n_q, n_heads, head_dim], token stride ld_q; k: dtype [n_k, n_heads, head_dim], token
+ *   stride ld_k; mass, mass_out: fp32 [n_heads, >= n_k], row stride ld_mass (both), may be the same
+ *   array, else must not overlap; entries from n_k on are left as they are.  decay is finite and >= 0;
+ *   0 starts over (mass is not read).  kv_bias: optional fp32 [n_heads, n_k], row stride ld_bias, as
+ *   the attention took it for this segment (finite values in [-64, 16], -inf excludes a key, whose
+ *   weight is then 0 whatever its key holds); any alignment.  softmax_scale 0 selects 1/sqrt(head_dim).
+ * ISPA_BF16: head_dim 64 or 128, else ISPA_ERR_UNSUPPORTED unless flags has ISPA_ATTN_CUDA_CORES, which
+ * admits 16 and 32 too.  ISPA_F32: head_dim 16, 32, 64 or 128, on CUDA cores.  Any alignment; bf16
+ * keys and queries at 16-byte aligned addresses with strides that are multiples of 8 run on the tensor
+ * cores when there are enough queries.  Deterministic.  n_k == 0 is a no-op; n_q == 0 only decays.
+ */
+ISPA_API ispa_status ispa_attn_mass(int32_t dtype, int32_t n_heads, int32_t head_dim, const void* q, int64_t n_q,
+                                    int64_t ld_q, const void* k, int64_t n_k, int64_t ld_k, const float* lse_loc,
+                                    const float* lse_hist, const float* kv_bias, int64_t ld_bias, float softmax_scale,
+                                    float decay, uint32_t flags, const float* mass, float* mass_out, int64_t ld_mass,
+                                    void* stream);
+
+/*
+ * ispa_cache_insert: n_new tokens enter a cache of `capacity` entries per head that holds n (the same
+ * for every head); per head the min(capacity, n + n_new) candidates of highest rank stay.  Candidates
+ * are the held entries in slot order, then the new tokens in token order.  Rank is the mass (NaN ranks
+ * as -inf), +inf for a protected position (pos < keep_below or pos >= keep_from); equal ranks stay in
+ * candidate order.  A held entry that stays keeps its slot.  The new tokens that stay take, in token
+ * order, the slots of the evicted entries in ascending order, then the slots from n on.  So slots are
+ * not in order of position once entries have left; attention over the cache does not depend on it.
+ *   k_cache, v_cache: dtype [capacity, n_heads, head_dim], token stride ld_cache; k_new, v_new: dtype
+ *   [n_new, n_heads, head_dim], token stride ld_new (not inside the cache); mass fp32 and pos int32
+ *   [n_heads, >= n], row stride ld_state; mass_new: fp32 [n_heads, n_new], row stride ld_mass_new, or
+ *   NULL for 0; the new tokens' positions are pos_new, pos_new + 1, ...; mass_out, pos_out: the state
+ *   after the call, [n_heads, >= min(capacity, n + n_new)], row stride ld_out: either the same arrays
+ *   (and strides) as mass and pos, or arrays that overlap none of the inputs.
+ * After the call every head holds min(capacity, n + n_new) entries; slots past that are left as they
+ * were.  Reads and writes only the rows of the new tokens that stay.  Any alignment (16-byte aligned
+ * rows copy faster).  head_dim 16, 32, 64 or 128; n_new <= 65536, else ISPA_ERR_UNSUPPORTED; n + n_new
+ * < 2^30; pos_new >= 0 and pos_new + n_new <= 2^31 - 1.  Deterministic.
+ */
+ISPA_API ispa_status ispa_cache_insert(int32_t dtype, int32_t n_heads, int32_t head_dim, void* k_cache, void* v_cache,
+                                       int64_t ld_cache, int64_t capacity, int64_t n, const float* mass,
+                                       const int32_t* pos, int64_t ld_state, const void* k_new, const void* v_new,
+                                       int64_t n_new, int64_t ld_new, const float* mass_new, int64_t ld_mass_new,
+                                       int32_t pos_new, int32_t keep_below, int32_t keep_from, float* mass_out,
+                                       int32_t* pos_out, int64_t ld_out, void* stream);
+
+/*
+ * Attention over history blocks that a cheap score selects: a long history stays in memory, and each
+ * group of queries reads only the blocks whose mean key points its way (FAST-AR's page, section 2 C,
+ * restricts each query to part of the keys; this library selects by block means, not by hashing).
+ *
+ * ispa_block_means: means[b, h, :] = the mean of the keys of block b (tokens b * block .. of k, the last
+ * block shorter when block does not divide n_k), fp32, for b = first_block .. ceil(n_k / block) - 1; a
+ * growing history passes the first block that its new tokens touch.  k: dtype [n_k, n_heads, head_dim],
+ * token stride ld_k; means: fp32 [blocks, n_heads, head_dim], block stride ld_means >= n_heads *
+ * head_dim; rows before first_block are left as they are.  Summed in 64 bits, rounded once.
+ */
+ISPA_API ispa_status ispa_block_means(int32_t dtype, int32_t n_heads, int32_t head_dim, const void* k, int64_t n_k,
+                                      int64_t ld_k, int32_t block, int64_t first_block, float* means,
+                                      int64_t ld_means, void* stream);
+
+/*
+ * ispa_block_select: for every head and group of q_block consecutive queries (the last group shorter),
+ * the n_sel blocks of highest score mean(q rows) . means[b, h, :], ties to the lowest block, written in
+ * ascending order to idx_out[h, group, 0..n_sel) (int32 [n_heads, ceil(n_q / q_block), n_sel], dense),
+ * -1 at the end where there are fewer blocks than n_sel.  A NaN score ranks as -inf.  Scores are
+ * formed in 64 bits, so the picks do not depend on the launch.  n_blocks <= 16384 and head_dim 16, 32,
+ * 64 or 128, else ISPA_ERR_UNSUPPORTED; q_block >= 1; n_sel >= 1.  n_q == 0 is a no-op.
+ */
+ISPA_API ispa_status ispa_block_select(int32_t dtype, int32_t n_heads, int32_t head_dim, const void* q, int64_t n_q,
+                                       int64_t ld_q, int32_t q_block, const float* means, int64_t n_blocks,
+                                       int64_t ld_means, int32_t n_sel, int32_t* idx_out, void* stream);
+
+/*
+ * ispa_block_sparse_attn: ispa_dual_stream_attn with the history branch over the listed blocks only.
+ * args: as there (five outputs, the same layouts); kv_bias must be NULL in every segment (else
+ * ISPA_ERR_UNSUPPORTED).  n_kv[ISPA_SEG_HIST] is the whole history's length.
+ *   idx: int32 [n_heads, ceil(n_q / q_block), n_sel], dense (device): the blocks of query group i are
+ *   idx[h, i, :], in any order; an entry outside 0 .. ceil(n_hist / block) - 1 names no block, a block
+ *   listed twice counts twice.  A row without any history key gets lse_hist = -inf, O_full = O_loc and
+ *   D = 0.  n_sel == 0 (idx unused) is attention over sink and local alone.
+ * Every entry of idx is read on the device when the kernel runs.  ISPA_BF16 with q_block a multiple of
+ * 128 runs on the tensor cores (block 64 or 128, head_dim 64 or 128 and the alignment rules of
+ * ispa_dual_stream_attn, else ISPA_ERR_UNSUPPORTED), ISPA_BF16 with q_block 1 (each query its own
+ * picks: the single-token form) on CUDA cores at any alignment; another q_block is
+ * ISPA_ERR_UNSUPPORTED.  ISPA_F32, or ISPA_BF16 with ISPA_ATTN_CUDA_CORES, runs on CUDA cores with any
+ * q_block >= 1, block of 1 to 65536, head_dim 16, 32, 64 or 128 and any alignment.
+ */
+ISPA_API ispa_status ispa_block_sparse_attn(const ispa_attn_args* args, const int32_t* idx, int32_t n_sel,
+                                            int32_t block, int32_t q_block, void* stream);
+
+/*
  * Instance-specific layer selection, ISPA section 2 "Dynamic Layer Selection" (host call, no GPU):
  * rank the n_layers values eps[] (host array) ascending and return the k lowest in idx_out[k]
  * (host), listed in ascending layer index.  Ties go to the lower layer index.  NaN ranks after

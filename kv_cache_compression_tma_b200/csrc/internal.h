@@ -170,6 +170,86 @@ struct TcMergeLaunch {
 bool tc_merge_supported(int64_t n_new);
 cudaError_t launch_tc_merge(const TcMergeLaunch& a, cudaStream_t s, int* n_launched);
 
+// ------------------------------------------------------------------ attention over selected blocks
+struct BlockList {
+  const int32_t* idx;  // [n_heads, groups, n_sel], entries outside [0, n_blocks) name no block
+  int n_sel, block, q_block;
+  int64_t groups;      // ceil(n_q / q_block)
+  int n_blocks;        // ceil(n_kv[history] / block)
+};
+// one row and head per cluster, CUDA cores (either dtype, any head_dim of the API, any alignment)
+cudaError_t launch_attn_blocks_rows(const AttnLaunch& a, const BlockList& b, cudaStream_t s, int* n_launched);
+
+struct BlockMeansLaunch {
+  int dtype;
+  const void* k;
+  int64_t n_k, ld_k;
+  int cols;  // n_heads * head_dim
+  int block;
+  int64_t first;
+  float* means;
+  int64_t ld_means;
+};
+cudaError_t launch_block_means(const BlockMeansLaunch& a, cudaStream_t s, int* n_launched);
+
+struct BlockSelectLaunch {
+  int dtype, n_heads, head_dim;
+  const void* q;
+  int64_t n_q, ld_q;
+  int q_block;
+  int64_t groups;
+  const float* means;
+  int n_blocks;
+  int64_t ld_means;
+  int n_sel;
+  int32_t* idx;
+};
+bool block_select_supported(int64_t n_blocks);
+cudaError_t launch_block_select(const BlockSelectLaunch& a, cudaStream_t s, int* n_launched);
+
+// ------------------------------------------------------------------ accumulated attention weight
+struct MassLaunch {
+  int dtype, n_heads, head_dim;
+  const void* q;
+  int64_t n_q, ld_q;
+  const void* k;
+  int64_t n_k, ld_k;
+  const float* lse_loc;   // [n_heads, n_q]
+  const float* lse_hist;  // same, or null
+  const float* bias;      // [n_heads, n_k] (row stride ld_bias), or null
+  int64_t ld_bias;
+  float scale, decay;
+  const float* mass;
+  float* mass_out;        // may be mass
+  int64_t ld_mass;        // of both
+  unsigned* status;
+};
+cudaError_t launch_mass_rows(const MassLaunch& a, cudaStream_t s, int* n_launched);
+
+// ------------------------------------------------------------------ cache insertion with eviction
+struct InsertLaunch {
+  int n_heads;
+  int row_bytes;  // head_dim elements
+  void* k;
+  void* v;
+  int64_t ld_cache_bytes;
+  int capacity, n, n_new;
+  const float* mass;
+  const int32_t* pos;
+  int64_t ld_state;
+  float* mass_out;  // may be mass
+  int32_t* pos_out;  // may be pos
+  int64_t ld_out;
+  const void* k_new;
+  const void* v_new;
+  int64_t ld_new_bytes;
+  const float* mass_new;  // or null: 0
+  int64_t ld_new_state;
+  int32_t pos_new, keep_below, keep_from;
+};
+bool cache_insert_supported(int64_t n, int64_t n_new);
+cudaError_t launch_cache_insert(const InsertLaunch& a, cudaStream_t s, int* n_launched);
+
 // driver entry point for cuTensorMapEncodeTiled (resolved once through the runtime)
 typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
                                   const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,

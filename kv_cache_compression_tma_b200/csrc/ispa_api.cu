@@ -47,6 +47,9 @@ void count(int n) { g_launches.fetch_add(static_cast<uint64_t>(n)); }
 
 bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
 
+// head dimensions of the kernels that spread a head's row over lanes
+bool rows_head_dim(int32_t hd) { return hd == 16 || hd == 32 || hd == 64 || hd == 128; }
+
 }  // namespace
 
 EncodeTiledFn get_encode_tiled() {
@@ -76,6 +79,73 @@ bool make_map_bf16_2d(CUtensorMap* map, const void* base, uint64_t rows, uint64_
   return r == CUDA_SUCCESS;
 }
 
+}  // namespace ispa
+
+namespace ispa {
+namespace {
+
+// Argument checks of an attention call and its launch description; `biased`: some segment has a bias.
+ispa_status fill_attn(const ispa_attn_args* a, AttnLaunch& L, bool& biased) {
+  biased = false;
+  if (!a) return ISPA_ERR_INVALID_ARG;
+  if (a->dtype != ISPA_BF16 && a->dtype != ISPA_F32) return ISPA_ERR_INVALID_ARG;
+  if (a->flags & ~1) return ISPA_ERR_INVALID_ARG;
+  if (a->n_heads < 1 || a->head_dim < 1) return ISPA_ERR_INVALID_ARG;
+  if (a->head_dim != 16 && a->head_dim != 32 && a->head_dim != 64 && a->head_dim != 128) return ISPA_ERR_UNSUPPORTED;
+  const int64_t d = static_cast<int64_t>(a->n_heads) * a->head_dim;
+  const int64_t lim = (1ll << 31) - 1;
+  if (a->n_q < 0 || a->n_q > lim) return ISPA_ERR_INVALID_ARG;
+  for (int s = 0; s < 3; ++s)
+    if (a->n_kv[s] < 0 || a->n_kv[s] > lim) return ISPA_ERR_INVALID_ARG;
+  if (a->n_kv[0] + a->n_kv[1] < 1) return ISPA_ERR_INVALID_ARG;
+  if (!(a->softmax_scale >= 0.f) || !isfinite(a->softmax_scale)) return ISPA_ERR_INVALID_ARG;
+  const size_t es = a->dtype == ISPA_BF16 ? 2 : 4;
+  if (a->n_q > 0) {
+    if (!a->q || !a->o_loc || !a->o_full || !a->lse_loc || !a->lse_hist) return ISPA_ERR_INVALID_ARG;
+    if (a->ld_q < d || a->ld_o < d) return ISPA_ERR_INVALID_ARG;
+    if (!aligned(a->q, es) || !aligned(a->o_loc, es) || !aligned(a->o_full, es) || !aligned(a->lse_loc, 4) ||
+        !aligned(a->lse_hist, 4) || (a->d_out && !aligned(a->d_out, es)))
+      return ISPA_ERR_INVALID_ARG;
+  }
+  for (int s = 0; s < 3; ++s) {
+    if (a->n_kv[s] == 0) continue;
+    if (!a->k[s] || !a->v[s] || a->ld_k[s] < d || a->ld_v[s] < d) return ISPA_ERR_INVALID_ARG;
+    if (!aligned(a->k[s], es) || !aligned(a->v[s], es)) return ISPA_ERR_INVALID_ARG;
+    if (a->kv_bias[s]) {
+      if (a->ld_bias[s] < a->n_kv[s] || !aligned(a->kv_bias[s], 4)) return ISPA_ERR_INVALID_ARG;
+      biased = true;
+    }
+  }
+  memset(&L, 0, sizeof(L));
+  L.dtype = a->dtype;
+  L.n_heads = a->n_heads;
+  L.head_dim = a->head_dim;
+  L.n_q = a->n_q;
+  L.q = a->q;
+  L.ld_q = a->ld_q;
+  for (int s = 0; s < 3; ++s) {
+    L.n_kv[s] = a->n_kv[s];
+    L.k[s] = a->k[s];
+    L.v[s] = a->v[s];
+    L.ld_k[s] = a->ld_k[s];
+    L.ld_v[s] = a->ld_v[s];
+  }
+  L.scale = a->softmax_scale > 0.f ? a->softmax_scale : 1.0f / sqrtf(static_cast<float>(a->head_dim));
+  L.o_loc = a->o_loc;
+  L.o_full = a->o_full;
+  L.d_out = a->d_out;
+  L.ld_o = a->ld_o;
+  L.lse_loc = a->lse_loc;
+  L.lse_hist = a->lse_hist;
+  L.test_flags = test_flags();
+  for (int s = 0; s < 3; ++s) {
+    L.bias[s] = a->n_kv[s] > 0 ? a->kv_bias[s] : nullptr;
+    L.ld_bias[s] = a->ld_bias[s];
+  }
+  return ISPA_OK;
+}
+
+}  // namespace
 }  // namespace ispa
 
 using namespace ispa;
@@ -109,64 +179,10 @@ const char* ispa_status_string(ispa_status s) {
 }
 
 ispa_status ispa_dual_stream_attn(const ispa_attn_args* a, void* stream) {
-  if (!a) return ISPA_ERR_INVALID_ARG;
-  if (a->dtype != ISPA_BF16 && a->dtype != ISPA_F32) return ISPA_ERR_INVALID_ARG;
-  if (a->flags & ~1) return ISPA_ERR_INVALID_ARG;
-  if (a->n_heads < 1 || a->head_dim < 1) return ISPA_ERR_INVALID_ARG;
-  if (a->head_dim != 16 && a->head_dim != 32 && a->head_dim != 64 && a->head_dim != 128) return ISPA_ERR_UNSUPPORTED;
-  const int64_t d = static_cast<int64_t>(a->n_heads) * a->head_dim;
-  const int64_t lim = (1ll << 31) - 1;
-  if (a->n_q < 0 || a->n_q > lim) return ISPA_ERR_INVALID_ARG;
-  for (int s = 0; s < 3; ++s)
-    if (a->n_kv[s] < 0 || a->n_kv[s] > lim) return ISPA_ERR_INVALID_ARG;
-  if (a->n_kv[0] + a->n_kv[1] < 1) return ISPA_ERR_INVALID_ARG;
-  if (!(a->softmax_scale >= 0.f) || !isfinite(a->softmax_scale)) return ISPA_ERR_INVALID_ARG;
-  const size_t es = a->dtype == ISPA_BF16 ? 2 : 4;
-  if (a->n_q > 0) {
-    if (!a->q || !a->o_loc || !a->o_full || !a->lse_loc || !a->lse_hist) return ISPA_ERR_INVALID_ARG;
-    if (a->ld_q < d || a->ld_o < d) return ISPA_ERR_INVALID_ARG;
-    if (!aligned(a->q, es) || !aligned(a->o_loc, es) || !aligned(a->o_full, es) || !aligned(a->lse_loc, 4) ||
-        !aligned(a->lse_hist, 4) || (a->d_out && !aligned(a->d_out, es)))
-      return ISPA_ERR_INVALID_ARG;
-  }
-  bool biased = false;
-  for (int s = 0; s < 3; ++s) {
-    if (a->n_kv[s] == 0) continue;
-    if (!a->k[s] || !a->v[s] || a->ld_k[s] < d || a->ld_v[s] < d) return ISPA_ERR_INVALID_ARG;
-    if (!aligned(a->k[s], es) || !aligned(a->v[s], es)) return ISPA_ERR_INVALID_ARG;
-    if (a->kv_bias[s]) {
-      if (a->ld_bias[s] < a->n_kv[s] || !aligned(a->kv_bias[s], 4)) return ISPA_ERR_INVALID_ARG;
-      biased = true;
-    }
-  }
-  if (a->n_q == 0) return ISPA_OK;
   AttnLaunch L;
-  memset(&L, 0, sizeof(L));
-  L.dtype = a->dtype;
-  L.n_heads = a->n_heads;
-  L.head_dim = a->head_dim;
-  L.n_q = a->n_q;
-  L.q = a->q;
-  L.ld_q = a->ld_q;
-  for (int s = 0; s < 3; ++s) {
-    L.n_kv[s] = a->n_kv[s];
-    L.k[s] = a->k[s];
-    L.v[s] = a->v[s];
-    L.ld_k[s] = a->ld_k[s];
-    L.ld_v[s] = a->ld_v[s];
-  }
-  L.scale = a->softmax_scale > 0.f ? a->softmax_scale : 1.0f / sqrtf(static_cast<float>(a->head_dim));
-  L.o_loc = a->o_loc;
-  L.o_full = a->o_full;
-  L.d_out = a->d_out;
-  L.ld_o = a->ld_o;
-  L.lse_loc = a->lse_loc;
-  L.lse_hist = a->lse_hist;
-  L.test_flags = test_flags();
-  for (int s = 0; s < 3; ++s) {
-    L.bias[s] = a->n_kv[s] > 0 ? a->kv_bias[s] : nullptr;
-    L.ld_bias[s] = a->ld_bias[s];
-  }
+  bool biased;
+  const ispa_status checked = fill_attn(a, L, biased);
+  if (checked != ISPA_OK || a->n_q == 0) return checked;
   // bf16 runs on the tensor cores or not at all, unless the caller asks for the CUDA-core kernel
   const bool cuda_cores = (a->flags & ISPA_ATTN_CUDA_CORES) != 0 || a->dtype == ISPA_F32;
   if (cuda_cores && biased) return ISPA_ERR_UNSUPPORTED;  // the CUDA-core kernel takes no bias
@@ -389,6 +405,131 @@ ispa_status ispa_tempcache_merge(int32_t n_heads, int32_t head_dim, void* k_cach
                   k_new, v_new, n_new, ld_new, idx, sim, threshold, st};
   int n = 0;
   cudaError_t e = launch_tc_merge(L, static_cast<cudaStream_t>(stream), &n);
+  count(n);
+  return e == cudaSuccess ? ISPA_OK : ISPA_ERR_CUDA;
+}
+
+ispa_status ispa_attn_mass(int32_t dtype, int32_t n_heads, int32_t head_dim, const void* q, int64_t n_q, int64_t ld_q,
+                           const void* k, int64_t n_k, int64_t ld_k, const float* lse_loc, const float* lse_hist,
+                           const float* kv_bias, int64_t ld_bias, float softmax_scale, float decay, uint32_t flags,
+                           const float* mass, float* mass_out, int64_t ld_mass, void* stream) {
+  if (dtype != ISPA_BF16 && dtype != ISPA_F32) return ISPA_ERR_INVALID_ARG;
+  if (flags & ~static_cast<uint32_t>(ISPA_ATTN_CUDA_CORES)) return ISPA_ERR_INVALID_ARG;
+  const int64_t lim = (1ll << 30);
+  if (n_heads < 1 || n_heads > 65535 || n_q < 0 || n_q > lim || n_k < 0 || n_k > lim) return ISPA_ERR_INVALID_ARG;
+  if (!rows_head_dim(head_dim)) return ISPA_ERR_UNSUPPORTED;
+  const bool cuda_cores = dtype == ISPA_F32 || (flags & ISPA_ATTN_CUDA_CORES) != 0;
+  if (!cuda_cores && head_dim < 64) return ISPA_ERR_UNSUPPORTED;
+  if (!(softmax_scale >= 0.f) || !isfinite(softmax_scale)) return ISPA_ERR_INVALID_ARG;
+  if (!(decay >= 0.f) || !isfinite(decay)) return ISPA_ERR_INVALID_ARG;
+  if (n_k == 0) return ISPA_OK;
+  const int64_t d = static_cast<int64_t>(n_heads) * head_dim;
+  const size_t es = dtype == ISPA_BF16 ? 2 : 4;
+  if (!k || !mass || !mass_out || ld_k < d || ld_mass < n_k) return ISPA_ERR_INVALID_ARG;
+  if (!aligned(k, es) || !aligned(mass, 4) || !aligned(mass_out, 4)) return ISPA_ERR_INVALID_ARG;
+  if (n_q > 0 && (!q || !lse_loc || ld_q < d || !aligned(q, es) || !aligned(lse_loc, 4) || (lse_hist && !aligned(lse_hist, 4))))
+    return ISPA_ERR_INVALID_ARG;
+  if (kv_bias && (ld_bias < n_k || !aligned(kv_bias, 4))) return ISPA_ERR_INVALID_ARG;
+  MassLaunch L{dtype, n_heads, head_dim, q, n_q, ld_q, k, n_k, ld_k, lse_loc, lse_hist, kv_bias, ld_bias,
+               softmax_scale > 0.f ? softmax_scale : 1.0f / sqrtf(static_cast<float>(head_dim)), decay, mass, mass_out,
+               ld_mass, status_ptr()};
+  if (!L.status) return ISPA_ERR_CUDA;
+  int n = 0;
+  cudaError_t e = launch_mass_rows(L, static_cast<cudaStream_t>(stream), &n);
+  count(n);
+  return e == cudaSuccess ? ISPA_OK : ISPA_ERR_CUDA;
+}
+
+ispa_status ispa_cache_insert(int32_t dtype, int32_t n_heads, int32_t head_dim, void* k_cache, void* v_cache,
+                              int64_t ld_cache, int64_t capacity, int64_t n, const float* mass, const int32_t* pos,
+                              int64_t ld_state, const void* k_new, const void* v_new, int64_t n_new, int64_t ld_new,
+                              const float* mass_new, int64_t ld_mass_new, int32_t pos_new, int32_t keep_below,
+                              int32_t keep_from, float* mass_out, int32_t* pos_out, int64_t ld_out, void* stream) {
+  if (dtype != ISPA_BF16 && dtype != ISPA_F32) return ISPA_ERR_INVALID_ARG;
+  if (n_heads < 1 || n_heads > 65535 || n < 0 || n_new < 0 || capacity < n || capacity >= (1ll << 30))
+    return ISPA_ERR_INVALID_ARG;
+  if (!rows_head_dim(head_dim)) return ISPA_ERR_UNSUPPORTED;
+  if (pos_new < 0 || pos_new > INT32_MAX - n_new) return ISPA_ERR_INVALID_ARG;
+  const int64_t d = static_cast<int64_t>(n_heads) * head_dim;
+  const int64_t total = std::min(capacity, n + n_new);
+  const size_t es = dtype == ISPA_BF16 ? 2 : 4;
+  if (total == 0) return ISPA_OK;
+  if (!mass || !pos || !mass_out || !pos_out || ld_state < n || ld_out < total) return ISPA_ERR_INVALID_ARG;
+  if (!aligned(mass, 4) || !aligned(pos, 4) || !aligned(mass_out, 4) || !aligned(pos_out, 4)) return ISPA_ERR_INVALID_ARG;
+  if ((mass_out == mass || pos_out == pos) && ld_out != ld_state) return ISPA_ERR_INVALID_ARG;
+  if (n_new > 0) {
+    if (!k_cache || !v_cache || !k_new || !v_new || ld_cache < d || ld_new < d) return ISPA_ERR_INVALID_ARG;
+    if (!aligned(k_cache, es) || !aligned(v_cache, es) || !aligned(k_new, es) || !aligned(v_new, es))
+      return ISPA_ERR_INVALID_ARG;
+    if (mass_new && (ld_mass_new < n_new || !aligned(mass_new, 4))) return ISPA_ERR_INVALID_ARG;
+  }
+  if (!cache_insert_supported(n, n_new)) return ISPA_ERR_UNSUPPORTED;
+  if (!status_ptr()) return ISPA_ERR_CUDA;
+  const int64_t bytes = static_cast<int64_t>(es);
+  InsertLaunch L{n_heads, static_cast<int>(head_dim * bytes), k_cache, v_cache, ld_cache * bytes,
+                 static_cast<int>(capacity), static_cast<int>(n), static_cast<int>(n_new), mass, pos, ld_state, mass_out,
+                 pos_out, ld_out, k_new, v_new, ld_new * bytes, mass_new, ld_mass_new, pos_new, keep_below, keep_from};
+  int launched = 0;
+  cudaError_t e = launch_cache_insert(L, static_cast<cudaStream_t>(stream), &launched);
+  count(launched);
+  return e == cudaSuccess ? ISPA_OK : ISPA_ERR_CUDA;
+}
+
+ispa_status ispa_block_means(int32_t dtype, int32_t n_heads, int32_t head_dim, const void* k, int64_t n_k, int64_t ld_k,
+                             int32_t block, int64_t first_block, float* means, int64_t ld_means, void* stream) {
+  if (dtype != ISPA_BF16 && dtype != ISPA_F32) return ISPA_ERR_INVALID_ARG;
+  if (n_heads < 1 || n_heads > 65535 || n_k < 0 || n_k > (1ll << 30) || block < 1 || first_block < 0) return ISPA_ERR_INVALID_ARG;
+  if (!rows_head_dim(head_dim)) return ISPA_ERR_UNSUPPORTED;
+  const int64_t d = static_cast<int64_t>(n_heads) * head_dim;
+  if (first_block >= (n_k + block - 1) / block) return ISPA_OK;
+  if (!k || !means || ld_k < d || ld_means < d) return ISPA_ERR_INVALID_ARG;
+  if (!aligned(k, dtype == ISPA_BF16 ? 2 : 4) || !aligned(means, 4)) return ISPA_ERR_INVALID_ARG;
+  if (!status_ptr()) return ISPA_ERR_CUDA;
+  BlockMeansLaunch L{dtype, k, n_k, ld_k, static_cast<int>(d), block, first_block, means, ld_means};
+  int n = 0;
+  cudaError_t e = launch_block_means(L, static_cast<cudaStream_t>(stream), &n);
+  count(n);
+  return e == cudaSuccess ? ISPA_OK : ISPA_ERR_CUDA;
+}
+
+ispa_status ispa_block_select(int32_t dtype, int32_t n_heads, int32_t head_dim, const void* q, int64_t n_q, int64_t ld_q,
+                              int32_t q_block, const float* means, int64_t n_blocks, int64_t ld_means, int32_t n_sel,
+                              int32_t* idx_out, void* stream) {
+  if (dtype != ISPA_BF16 && dtype != ISPA_F32) return ISPA_ERR_INVALID_ARG;
+  if (n_heads < 1 || n_heads > 65535 || n_q < 0 || n_q > (1ll << 30) || q_block < 1 || n_blocks < 0 || n_sel < 1)
+    return ISPA_ERR_INVALID_ARG;
+  if (!rows_head_dim(head_dim) || !block_select_supported(n_blocks)) return ISPA_ERR_UNSUPPORTED;
+  if (n_q == 0) return ISPA_OK;
+  const int64_t d = static_cast<int64_t>(n_heads) * head_dim;
+  if (!q || !idx_out || ld_q < d || !aligned(q, dtype == ISPA_BF16 ? 2 : 4) || !aligned(idx_out, 4)) return ISPA_ERR_INVALID_ARG;
+  if (n_blocks > 0 && (!means || ld_means < d || !aligned(means, 4))) return ISPA_ERR_INVALID_ARG;
+  if (!status_ptr()) return ISPA_ERR_CUDA;
+  BlockSelectLaunch L{dtype, n_heads, head_dim, q, n_q, ld_q, q_block, (n_q + q_block - 1) / q_block, means,
+                      static_cast<int>(n_blocks), ld_means, n_sel, idx_out};
+  int n = 0;
+  cudaError_t e = launch_block_select(L, static_cast<cudaStream_t>(stream), &n);
+  count(n);
+  return e == cudaSuccess ? ISPA_OK : ISPA_ERR_CUDA;
+}
+
+ispa_status ispa_block_sparse_attn(const ispa_attn_args* a, const int32_t* idx, int32_t n_sel, int32_t block,
+                                   int32_t q_block, void* stream) {
+  AttnLaunch L;
+  bool biased;
+  const ispa_status checked = fill_attn(a, L, biased);
+  if (checked != ISPA_OK) return checked;
+  if (n_sel < 0 || block < 1 || block > 65536 || q_block < 1 || a->n_heads > 65535) return ISPA_ERR_INVALID_ARG;
+  if (n_sel > 0 && (!idx || !aligned(idx, 4))) return ISPA_ERR_INVALID_ARG;
+  if (biased) return ISPA_ERR_UNSUPPORTED;
+  const bool cuda_cores = (a->flags & ISPA_ATTN_CUDA_CORES) != 0 || a->dtype == ISPA_F32;
+  if (!cuda_cores && q_block != 1) return ISPA_ERR_UNSUPPORTED;
+  if (a->n_q == 0) return ISPA_OK;
+  const BlockList B{idx, n_sel, block, q_block, (a->n_q + q_block - 1) / q_block,
+                    static_cast<int>((a->n_kv[ISPA_SEG_HIST] + block - 1) / block)};
+  L.status = status_ptr();
+  if (!L.status) return ISPA_ERR_CUDA;
+  int n = 0;
+  cudaError_t e = launch_attn_blocks_rows(L, B, static_cast<cudaStream_t>(stream), &n);
   count(n);
   return e == cudaSuccess ? ISPA_OK : ISPA_ERR_CUDA;
 }

@@ -1,0 +1,23 @@
+// mass.cuh -- the two scalar rules of the accumulated attention weight, shared by its kernels.
+#pragma once
+
+#include <math.h>
+
+namespace ispa {
+
+// log-sum-exp of a query row over both branches; +inf for a row without any key (both -inf), so that
+// exp(s - L) gives every key 0 from it.
+__device__ __forceinline__ float mass_row_lse(float lse_loc, float lse_hist) {
+  const float hi = fmaxf(lse_loc, lse_hist);
+  if (hi == -INFINITY) return INFINITY;
+  return hi + log1pf(expf(-fabsf(lse_loc - lse_hist)));
+}
+
+// A key's bias is common to all its terms, so it multiplies the sum.  The terms stay finite for the
+// biases the attention admits: L covers the key itself, so s - L <= -b <= 64.  An excluded key
+// (bias -inf) is in no row's L, and its sum may be anything: it gets 0 whatever the sum is.
+__device__ __forceinline__ float mass_apply_bias(float sum, float bias) {
+  return bias == -INFINITY ? 0.f : sum * expf(bias);
+}
+
+}  // namespace ispa

@@ -27,7 +27,8 @@ ISPA_QUANT_COLUMNS = 0x1
 
 SYMBOLS = ("ispa_dual_stream_attn", "ispa_accum_stats", "ispa_absorb_workspace_size", "ispa_absorb",
            "ispa_absorb_static", "ispa_project", "ispa_quantize_e4m3", "ispa_project_w8a8", "ispa_tempcache_match",
-           "ispa_tempcache_merge", "ispa_select_layers",
+           "ispa_tempcache_merge", "ispa_attn_mass", "ispa_cache_insert", "ispa_block_means", "ispa_block_select",
+           "ispa_block_sparse_attn", "ispa_select_layers",
            "ispa_get_device_status",
            "ispa_peek_device_status_bits", "ispa_test_set_flags",
            "ispa_status_string", "ispa_version", "ispa_launch_count")
@@ -92,6 +93,14 @@ def lib() -> ctypes.CDLL:
                                            ctypes.c_void_p, ctypes.c_void_p, ctypes.c_int64, ctypes.c_void_p,
                                            ctypes.c_void_p, ctypes.c_void_p, ctypes.c_int64, ctypes.c_int64,
                                            ctypes.c_void_p, ctypes.c_void_p, ctypes.c_float, ctypes.c_void_p]
+        c32, c64, vp = ctypes.c_int32, ctypes.c_int64, ctypes.c_void_p
+        L.ispa_attn_mass.argtypes = [c32, c32, c32, vp, c64, c64, vp, c64, c64, vp, vp, vp, c64, ctypes.c_float,
+                                     ctypes.c_float, ctypes.c_uint32, vp, vp, c64, vp]
+        L.ispa_cache_insert.argtypes = [c32, c32, c32, vp, vp, c64, c64, c64, vp, vp, c64, vp, vp, c64, c64, vp, c64,
+                                        c32, c32, c32, vp, vp, c64, vp]
+        L.ispa_block_means.argtypes = [c32, c32, c32, vp, c64, c64, c32, c64, vp, c64, vp]
+        L.ispa_block_select.argtypes = [c32, c32, c32, vp, c64, c64, c32, vp, c64, c64, c32, vp, vp]
+        L.ispa_block_sparse_attn.argtypes = [ctypes.POINTER(AttnArgs), vp, c32, c32, c32, vp]
         L.ispa_select_layers.argtypes = [ctypes.POINTER(ctypes.c_double), ctypes.c_int32, ctypes.c_int32,
                                          ctypes.POINTER(ctypes.c_int32), ctypes.POINTER(ctypes.c_uint8)]
         L.ispa_get_device_status.argtypes = [ctypes.c_void_p]
@@ -104,7 +113,8 @@ def lib() -> ctypes.CDLL:
         for name in ("ispa_dual_stream_attn", "ispa_accum_stats", "ispa_absorb_workspace_size", "ispa_absorb",
                      "ispa_absorb_static", "ispa_select_layers", "ispa_get_device_status", "ispa_peek_device_status_bits",
                      "ispa_test_set_flags", "ispa_quantize_e4m3", "ispa_project_w8a8", "ispa_tempcache_match",
-                     "ispa_tempcache_merge"):
+                     "ispa_tempcache_merge", "ispa_attn_mass", "ispa_cache_insert", "ispa_block_means",
+                     "ispa_block_select", "ispa_block_sparse_attn"):
             getattr(L, name).restype = ctypes.c_int32
         _lib = L
     return _lib
@@ -164,16 +174,9 @@ def _row_stride(t, what: str) -> int:
     return int(t.stride(0))
 
 
-def dual_stream_attn(q, k_sink, v_sink, k_loc, v_loc, k_hist, v_hist, *, o_loc=None, o_full=None, lse_loc=None,
-                     lse_hist=None, d_out=None, want_delta: bool = True, softmax_scale: float = 0.0,
-                     cuda_cores: bool = False, kv_bias=(None, None, None), stream=None) -> dict:
-    """ispa_dual_stream_attn on torch CUDA tensors.
-
-    q, k_*, v_*: [tokens, H, hd] (bf16 or fp32).  Outputs (allocated if not given): o_loc, o_full and
-    (if want_delta) d = O_full - O_loc as [n_q, H*hd] in q's dtype; lse_loc, lse_hist fp32 [H, n_q].
-    kv_bias: optional per-segment fp32 [H, n_kv] additive logit biases (natural log), e.g. the log group
-    sizes of a TempCache-merged history.
-    """
+def _attn_args(q, k_sink, v_sink, k_loc, v_loc, k_hist, v_hist, o_loc, o_full, lse_loc, lse_hist, d_out, want_delta,
+               softmax_scale, cuda_cores, kv_bias):
+    """The argument block of an attention call, and its outputs (allocated where not given)."""
     import torch
     _on_current_device(q, k_sink, v_sink, k_loc, v_loc, k_hist, v_hist, o_loc, o_full, lse_loc, lse_hist, d_out,
                        *kv_bias)
@@ -213,8 +216,23 @@ def dual_stream_attn(q, k_sink, v_sink, k_loc, v_loc, k_hist, v_hist, *, o_loc=N
             if bt.dtype != torch.float32 or bt.dim() != 2 or bt.stride(1) != 1:
                 raise ValueError("kv_bias entries must be fp32 [H, n_kv] with contiguous columns")
             a.kv_bias[i], a.ld_bias[i] = _ptr(bt), int(bt.stride(0))
+    return a, {"o_loc": o_loc, "o_full": o_full, "d": d_out, "lse_loc": lse_loc, "lse_hist": lse_hist}
+
+
+def dual_stream_attn(q, k_sink, v_sink, k_loc, v_loc, k_hist, v_hist, *, o_loc=None, o_full=None, lse_loc=None,
+                     lse_hist=None, d_out=None, want_delta: bool = True, softmax_scale: float = 0.0,
+                     cuda_cores: bool = False, kv_bias=(None, None, None), stream=None) -> dict:
+    """ispa_dual_stream_attn on torch CUDA tensors.
+
+    q, k_*, v_*: [tokens, H, hd] (bf16 or fp32).  Outputs (allocated if not given): o_loc, o_full and
+    (if want_delta) d = O_full - O_loc as [n_q, H*hd] in q's dtype; lse_loc, lse_hist fp32 [H, n_q].
+    kv_bias: optional per-segment fp32 [H, n_kv] additive logit biases (natural log), e.g. the log group
+    sizes of a TempCache-merged history.
+    """
+    a, out = _attn_args(q, k_sink, v_sink, k_loc, v_loc, k_hist, v_hist, o_loc, o_full, lse_loc, lse_hist, d_out,
+                        want_delta, softmax_scale, cuda_cores, kv_bias)
     _check(lib().ispa_dual_stream_attn(ctypes.byref(a), _stream(stream)), "ispa_dual_stream_attn")
-    return {"o_loc": o_loc, "o_full": o_full, "d": d_out, "lse_loc": lse_loc, "lse_hist": lse_hist}
+    return out
 
 
 def accum_stats(a_loc, a_second, G, R, S, *, second_is_full: bool = False, zero: bool = False, stream=None):
@@ -393,6 +411,184 @@ class TempCache:
         """(k, v, bias) views of the live bound, for dual_stream_attn's history segment."""
         n = self.n_cache
         return self.k[:n], self.v[:n], self.bias[:, :n]
+
+
+def _state_stride(t, what: str, heads: int, cols: int, dtype) -> int:
+    """Row stride of a per-head state array [H, >= cols] with contiguous columns."""
+    if t.dim() != 2 or t.dtype != dtype or t.shape[0] != heads or t.shape[1] < cols or (t.shape[1] > 1 and t.stride(1) != 1):
+        raise ValueError(f"{what}: expected {dtype} [{heads}, >= {cols}] with contiguous columns")
+    return int(t.stride(0)) if heads > 1 else max(int(t.shape[1]), 1)
+
+
+def _heads_like(t, what: str, heads: int, head_dim: int, dtype):
+    if t.dim() != 3 or t.shape[1] != heads or t.shape[2] != head_dim or t.dtype != dtype:
+        raise ValueError(f"{what}: expected {dtype} [tokens, {heads}, {head_dim}]")
+
+
+def attn_mass(q, k, lse_loc, lse_hist, mass, *, kv_bias=None, decay: float = 1.0, softmax_scale: float = 0.0,
+              cuda_cores: bool = False, mass_out=None, stream=None):
+    """ispa_attn_mass: mass[h, j] = decay * mass[h, j] + the attention weight that key j collects from the
+    queries q [n_q, H, hd], for the keys k [n_k, H, hd] of one segment.  lse_loc, lse_hist: fp32 [H, n_q],
+    contiguous, as dual_stream_attn returned them for the same queries (lse_hist None: no history branch).
+    kv_bias: fp32 [H, >= n_k], the segment's bias in that call.  mass fp32 [H, >= n_k]; the result goes to
+    mass_out (same shape and stride as mass) or back into mass.  Returns the array written."""
+    import torch
+    _on_current_device(q, k, lse_loc, lse_hist, mass, kv_bias, mass_out)
+    n_q, H, hd = q.shape
+    n_k = k.shape[0]
+    _heads_like(k, "k", H, hd, q.dtype)
+    for t in (lse_loc, lse_hist):
+        if t is not None and (t.dtype != torch.float32 or tuple(t.shape) != (H, n_q) or not t.is_contiguous()):
+            raise ValueError("lse_loc and lse_hist must be contiguous fp32 [H, n_q]")
+    ld_mass = _state_stride(mass, "mass", H, n_k, torch.float32)
+    if mass_out is None:
+        mass_out = mass
+    elif _state_stride(mass_out, "mass_out", H, n_k, torch.float32) != ld_mass:
+        raise ValueError("mass and mass_out must share a row stride")
+    ld_bias = 0 if kv_bias is None else _state_stride(kv_bias, "kv_bias", H, n_k, torch.float32)
+    _check(lib().ispa_attn_mass(_dtype_code(q), H, hd, _ptr(q), n_q, _row_stride(q, "q"), _ptr(k), n_k,
+                                _row_stride(k, "k"), _ptr(lse_loc), _ptr(lse_hist), _ptr(kv_bias), ld_bias,
+                                softmax_scale, decay, ISPA_ATTN_CUDA_CORES if cuda_cores else 0, _ptr(mass),
+                                _ptr(mass_out), ld_mass, _stream(stream)), "ispa_attn_mass")
+    return mass_out
+
+
+INT32_MAX = 2 ** 31 - 1
+
+
+def cache_insert(k_cache, v_cache, mass, pos, n: int, k_new, v_new, mass_new, pos_new: int, *, keep_below: int = 0,
+                 keep_from: int = INT32_MAX, mass_out=None, pos_out=None, stream=None) -> int:
+    """ispa_cache_insert: the new tokens k_new, v_new [n_new, H, hd] with weights mass_new (fp32 [H, n_new],
+    None = 0) at positions pos_new, pos_new + 1, ... enter the cache k_cache, v_cache [capacity, H, hd] that
+    holds n entries per head with weights mass (fp32 [H, >= n]) and positions pos (int32); the entries
+    of least weight leave.  Positions below keep_below or from keep_from on are protected.  The state
+    goes to mass_out, pos_out or back into mass, pos.  Returns the number of entries held afterwards."""
+    import torch
+    _on_current_device(k_cache, v_cache, mass, pos, k_new, v_new, mass_new, mass_out, pos_out)
+    capacity, H, hd = k_cache.shape
+    n_new = k_new.shape[0]
+    total = min(capacity, n + n_new)
+    for t, what in ((v_cache, "v_cache"), (k_new, "k_new"), (v_new, "v_new")):
+        _heads_like(t, what, H, hd, k_cache.dtype)
+    if v_cache.shape[0] != capacity or v_new.shape[0] != n_new:
+        raise ValueError("k and v must have the same number of tokens")
+    ld_cache, ld_new = _row_stride(k_cache, "k_cache"), _row_stride(k_new, "k_new")
+    if _row_stride(v_cache, "v_cache") != ld_cache or _row_stride(v_new, "v_new") != ld_new:
+        raise ValueError("k and v must share a row stride")
+    mass_out = mass if mass_out is None else mass_out
+    pos_out = pos if pos_out is None else pos_out
+    ld_state = _state_stride(mass, "mass", H, n, torch.float32)
+    ld_out = _state_stride(mass_out, "mass_out", H, total, torch.float32)
+    if _state_stride(pos, "pos", H, n, torch.int32) != ld_state or _state_stride(pos_out, "pos_out", H, total, torch.int32) != ld_out:
+        raise ValueError("mass and pos (mass_out and pos_out) must share a row stride")
+    ld_mass_new = 0 if mass_new is None else _state_stride(mass_new, "mass_new", H, n_new, torch.float32)
+    _check(lib().ispa_cache_insert(_dtype_code(k_cache), H, hd, _ptr(k_cache), _ptr(v_cache), ld_cache, capacity, n,
+                                   _ptr(mass), _ptr(pos), ld_state, _ptr(k_new), _ptr(v_new), n_new, ld_new,
+                                   _ptr(mass_new), ld_mass_new, pos_new, keep_below, keep_from, _ptr(mass_out),
+                                   _ptr(pos_out), ld_out, _stream(stream)), "ispa_cache_insert")
+    return total
+
+
+class MassCache:
+    """A KV segment of at most `capacity` entries per head, kept by accumulated attention weight: every
+    attention call over it may add the weights its keys collected (accumulate), and new tokens push out
+    the entries of least weight (insert); see ispa_attn_mass / ispa_cache_insert in include/ispa.h."""
+
+    def __init__(self, n_heads: int, head_dim: int, capacity: int, dtype=None, device="cuda"):
+        import torch
+        self.n_heads, self.head_dim, self.capacity = n_heads, head_dim, capacity
+        self.k = torch.zeros((capacity, n_heads, head_dim), dtype=dtype or torch.bfloat16, device=device)
+        self.v = torch.zeros_like(self.k)
+        self.mass = torch.zeros((n_heads, capacity), dtype=torch.float32, device=device)
+        self.pos = torch.zeros((n_heads, capacity), dtype=torch.int32, device=device)
+        self.n = 0     # entries held, the same for every head
+        self.seen = 0  # tokens inserted so far: the next token's position
+
+    def segment(self):
+        """(k, v) views of the held entries, for dual_stream_attn's history segment."""
+        return self.k[:self.n], self.v[:self.n]
+
+    def accumulate(self, q, lse_loc, lse_hist=None, *, decay: float = 1.0, softmax_scale: float = 0.0, stream=None):
+        """Add the weights that the held keys collected from q in the attention call that gave the lse's."""
+        attn_mass(q, self.k[:self.n], lse_loc, lse_hist, self.mass, decay=decay, softmax_scale=softmax_scale,
+                  stream=stream)
+
+    def insert(self, k_new, v_new, mass_new=None, *, first: int = 0, recent: int = 0, stream=None):
+        """Insert a frame's tokens; the first `first` positions of the stream and its newest `recent`
+        tokens are protected."""
+        n_new = k_new.shape[0]
+        keep_from = max(0, self.seen + n_new - recent) if recent > 0 else INT32_MAX
+        self.n = cache_insert(self.k, self.v, self.mass, self.pos, self.n, k_new, v_new, mass_new, self.seen,
+                              keep_below=first, keep_from=keep_from, stream=stream)
+        self.seen += n_new
+
+
+def block_means(k, means, block: int, *, first: int = 0, stream=None):
+    """ispa_block_means: means[b] (fp32 [>= blocks, H, hd]) = mean key of block b of k [n_k, H, hd], for the
+    blocks from `first` on; earlier rows are left as they are."""
+    import torch
+    _on_current_device(k, means)
+    n_k, H, hd = k.shape
+    _heads_like(means, "means", H, hd, torch.float32)
+    if means.shape[0] < -(-n_k // block):
+        raise ValueError("means has fewer rows than k has blocks")
+    _check(lib().ispa_block_means(_dtype_code(k), H, hd, _ptr(k), n_k, _row_stride(k, "k"), block, first, _ptr(means),
+                                  _row_stride(means, "means"), _stream(stream)), "ispa_block_means")
+    return means
+
+
+def block_select(q, means, n_sel: int, *, q_block: int = 1, out=None, stream=None):
+    """ispa_block_select: int32 [H, ceil(n_q / q_block), n_sel], the blocks (rows of means, fp32 [blocks, H,
+    hd]) of highest (mean query of the group) . (mean key), ascending, -1 where there are fewer."""
+    import torch
+    _on_current_device(q, means, out)
+    n_q, H, hd = q.shape
+    _heads_like(means, "means", H, hd, torch.float32)
+    shape = (H, -(-n_q // q_block), n_sel)
+    if out is None:
+        out = torch.empty(shape, dtype=torch.int32, device=q.device)
+    elif out.dtype != torch.int32 or tuple(out.shape) != shape or not out.is_contiguous():
+        raise ValueError(f"out must be contiguous int32 {list(shape)}")
+    _check(lib().ispa_block_select(_dtype_code(q), H, hd, _ptr(q), n_q, _row_stride(q, "q"), q_block, _ptr(means),
+                                   means.shape[0], _row_stride(means, "means"), n_sel, _ptr(out), _stream(stream)),
+           "ispa_block_select")
+    return out
+
+
+class BlockIndex:
+    """The mean keys of a growing history's blocks, and the selection of blocks by them; see
+    ispa_block_means / ispa_block_select in include/ispa.h."""
+
+    def __init__(self, n_heads: int, head_dim: int, max_tokens: int, block: int = 128, device="cuda"):
+        import torch
+        self.block, self.n = block, 0
+        self.means = torch.zeros((-(-max_tokens // block), n_heads, head_dim), dtype=torch.float32, device=device)
+
+    def extend(self, k, stream=None):
+        """Pool the blocks of the history k [n, H, hd] that its tokens since the last call touch."""
+        block_means(k, self.means, self.block, first=self.n // self.block, stream=stream)
+        self.n = k.shape[0]
+
+    def select(self, q, n_sel: int, *, q_block: int = 1, out=None, stream=None):
+        return block_select(q, self.means[:-(-self.n // self.block)], n_sel, q_block=q_block, out=out, stream=stream)
+
+
+def block_sparse_attn(q, k_sink, v_sink, k_loc, v_loc, k_hist, v_hist, idx, *, block: int, q_block: int = 1, o_loc=None,
+                      o_full=None, lse_loc=None, lse_hist=None, d_out=None, want_delta: bool = True,
+                      softmax_scale: float = 0.0, cuda_cores: bool = False, stream=None) -> dict:
+    """ispa_block_sparse_attn: dual_stream_attn whose history branch covers only the blocks (of `block`
+    tokens of k_hist, v_hist) listed in idx, int32 [H, ceil(n_q / q_block), n_sel], for each group of
+    q_block queries (as block_select gives them).  The same outputs as dual_stream_attn."""
+    import torch
+    a, out = _attn_args(q, k_sink, v_sink, k_loc, v_loc, k_hist, v_hist, o_loc, o_full, lse_loc, lse_hist, d_out,
+                        want_delta, softmax_scale, cuda_cores, (None, None, None))
+    _on_current_device(idx)
+    groups = -(-a.n_q // q_block)
+    if idx.dtype != torch.int32 or idx.dim() != 3 or tuple(idx.shape[:2]) != (a.n_heads, groups) or not idx.is_contiguous():
+        raise ValueError(f"idx must be contiguous int32 [{a.n_heads}, {groups}, n_sel]")
+    _check(lib().ispa_block_sparse_attn(ctypes.byref(a), _ptr(idx), idx.shape[2], block, q_block, _stream(stream)),
+           "ispa_block_sparse_attn")
+    return out
 
 
 def select_layers(eps: Sequence[float], k: int):

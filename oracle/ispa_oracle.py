@@ -48,6 +48,7 @@ __all__ = [
     "softmax_attention", "dual_stream", "stack_heads", "sufficient_stats", "ridge_lambda", "absorb",
     "reconstruction_error", "error_from_stats", "select_layers", "update_weight", "lse_merge",
     "biased_softmax_attention", "tempcache_match", "tempcache_merge",
+    "attn_mass", "cache_insert", "block_means", "block_select", "block_sparse",
 ]
 
 # rows handled per numpy call; each query row is computed independently, this only bounds memory
@@ -374,3 +375,98 @@ def tempcache_merge(k_cache, v_cache, count, k_new, v_new, idx, sim, threshold: 
         grown = (c_out[h, :N] > count[h]) & (count[h] > 0)
         v_out[:N, h][grown] = sums[grown] / c_out[h, :N][grown][:, None]
     return k_out, v_out, c_out
+
+
+# ------------------------------------------------------------------ bounded histories
+def attn_mass(q, k, lse_loc, lse_hist, mass, decay: float = 1.0, bias=None, scale: Optional[float] = None):
+    """decay * mass + the softmax weight each key collects: q [n_q, H, hd], k [n_k, H, hd], lse_* [H, n_q]
+    (lse_hist None: no history branch), mass [H, n_k], bias [H, n_k] or None.  The weight of key j in row
+    i is exp(scale q_i.k_j + bias_j) / (exp(lse_loc_i) + exp(lse_hist_i)); an excluded key (bias -inf)
+    and a row without keys (both -inf) give 0."""
+    q, k = np.asarray(q, np.float64), np.asarray(k, np.float64)
+    n_q, H, hd = q.shape
+    scale = 1.0 / math.sqrt(hd) if scale is None else scale
+    out = np.zeros((H, k.shape[0])) if decay == 0.0 else decay * np.asarray(mass, np.float64)
+    for h in range(H):
+        live = np.ones(k.shape[0], bool) if bias is None else ~np.isneginf(bias[h])
+        b = 0.0 if bias is None else np.asarray(bias[h], np.float64)[live]
+        for i in range(n_q):
+            L = float(lse_loc[h, i]) if lse_hist is None else np.logaddexp(float(lse_loc[h, i]), float(lse_hist[h, i]))
+            if np.isneginf(L):
+                continue
+            out[h, live] += np.exp(scale * (k[live, h] @ q[i, h]) + b - L)
+    return out
+
+
+def cache_insert(mass, pos, mass_new, pos_new: int, capacity: int, keep_below: int, keep_from: int):
+    """Per head, which candidate (held entries 0..n-1, then new tokens n..n+n_new-1) ends in each slot of
+    the cache: int64 [H, min(capacity, n + n_new)].  mass, pos [H, n]; mass_new [H, n_new]."""
+    mass, pos, mass_new = np.asarray(mass, np.float64), np.asarray(pos), np.asarray(mass_new, np.float64)
+    H, n = mass.shape
+    n_new = mass_new.shape[1]
+    total = min(capacity, n + n_new)
+    src = np.zeros((H, total), dtype=np.int64)
+    for h in range(H):
+        cand = []
+        for c in range(n + n_new):
+            m = mass[h, c] if c < n else mass_new[h, c - n]
+            p = int(pos[h, c]) if c < n else pos_new + c - n
+            r = math.inf if (p < keep_below or p >= keep_from) else (-math.inf if math.isnan(m) else float(m))
+            cand.append((-r, c))
+        stay = sorted(c for _, c in sorted(cand)[:total])
+        slots = [0] * total
+        held = set(c for c in stay if c < n)
+        free = iter([s for s in range(total) if s >= n or s not in held])
+        for c in held:
+            slots[c] = c
+        for c in stay:
+            if c >= n:
+                slots[next(free)] = c
+        src[h] = slots
+    return src
+
+
+def block_means(k, block: int):
+    """Mean key of each block of `block` tokens of k [n_k, H, hd] (the last one shorter), fp64."""
+    k = np.asarray(k, np.float64)
+    return np.stack([k[b:b + block].mean(axis=0) for b in range(0, k.shape[0], block)]) if k.shape[0] else \
+        np.zeros((0,) + k.shape[1:])
+
+
+def block_select(q, means, n_sel: int, q_block: int):
+    """int64 [H, groups, n_sel]: per head and group of q_block rows the blocks of highest (mean query) .
+    (mean key), ascending, ties to the lowest block, NaN ranked as -inf, -1 where there are fewer."""
+    q, means = np.asarray(q, np.float64), np.asarray(means, np.float64)
+    n_q, H, _ = q.shape
+    groups = -(-n_q // q_block)
+    out = np.full((H, groups, n_sel), -1, dtype=np.int64)
+    for h in range(H):
+        for g in range(groups):
+            score = means[:, h] @ q[g * q_block:(g + 1) * q_block, h].mean(axis=0)
+            score = np.where(np.isnan(score), -np.inf, score)
+            best = np.sort(np.argsort(-score, kind="stable")[:n_sel])
+            out[h, g, :len(best)] = best
+    return out
+
+
+def block_sparse(q, k_sink, v_sink, k_loc, v_loc, k_hist, v_hist, idx, block: int, q_block: int):
+    """dual_stream whose history keys are, per head and group of rows, those of the blocks idx[h, g] (entries
+    that name no block are skipped): the same dict of O_loc, O_full, lse_loc, lse_hist, lse_full."""
+    n_q, H, hd = np.asarray(q).shape
+    n_hist = np.asarray(k_hist).shape[0]
+    out = {w: np.zeros((n_q, H, hd)) for w in ("O_loc", "O_full")}
+    out.update({w: np.zeros((H, n_q)) for w in ("lse_loc", "lse_hist", "lse_full")})
+    scale = 1.0 / math.sqrt(hd)
+    kl = np.concatenate([k_sink, k_loc]).astype(np.float64)
+    vl = np.concatenate([v_sink, v_loc]).astype(np.float64)
+    for h in range(H):
+        for g in range(np.asarray(idx).shape[1]):
+            r = slice(g * q_block, min(n_q, (g + 1) * q_block))
+            keys = [j for b in idx[h, g] if 0 <= b and int(b) * block < n_hist
+                    for j in range(int(b) * block, min(n_hist, (int(b) + 1) * block))]
+            kh, vh = np.asarray(k_hist, np.float64)[keys, h], np.asarray(v_hist, np.float64)[keys, h]
+            out["O_loc"][r, h], out["lse_loc"][h, r] = softmax_attention(q[r, h], kl[:, h], vl[:, h], scale)
+            out["O_full"][r, h], out["lse_full"][h, r] = softmax_attention(
+                q[r, h], np.concatenate([kl[:, h], kh]), np.concatenate([vl[:, h], vh]), scale)
+            out["lse_hist"][h, r] = softmax_attention(q[r, h], kh, vh, scale)[1] if keys else -np.inf
+    return out

@@ -1,0 +1,403 @@
+"""The bounded-history operators on the GPU against the fp64 oracle: accumulated attention weight, cache
+insertion with eviction, block means, block selection and dual-stream attention over selected blocks.
+
+Tolerances.  Selections, positions and copied rows are exact.  Block means: the fp64 mean rounded once
+(2^-24; the 64-bit sums of the two sides differ by far less).  Attention weights: a logit is a sum of
+hd <= 128 products of size |q k| / sqrt(hd) (q of deviation 2, so about 14.5 in all) with roundings of
+2^-24 of the running sum each: a random walk of sqrt(128) 2^-24 14.5 = 1e-5, plus 2^-24 of |logit| + |L|
+<= 60 in the exponent (4e-6) and the exponential's 2^-22; per key that is below 3e-5 relative, and zeros
+are exact.  bf16 outputs of the row kernel: one rounding, 2^-8 of each value, so 2^-8 of the norm, plus
+2e-5 of arithmetic; tensor cores: the repository's attention tolerances (P is rounded to bf16 too)."""
+import numpy as np
+import pytest
+
+import ispa_inputs as inp
+from oracle import ispa_oracle as orc
+from gpu_helpers import ATTN_TOL, host, rel
+
+pytestmark = pytest.mark.gpu
+
+MASS_TOL = 3e-5
+ROW_TOL = {"o_loc": 2.0 ** -8 + 2e-5, "o_full": 2.0 ** -8 + 2e-5, "d": 2.0 ** -8 + 2e-5, "lse_loc": 5e-5, "lse_hist": 5e-5}
+F32_TOL = {"o_loc": 2e-5, "o_full": 2e-5, "d": 4e-5, "lse_loc": 5e-5, "lse_hist": 5e-5}
+
+
+def tensor(shape, seed, dtype, sc=1.0, pad=0, lead=0):
+    """Seeded [tokens, H, hd] values on the GPU, rounded to dtype, as a view of a wider row (pad elements)
+    that starts `lead` elements into its storage."""
+    import torch
+    x = inp.gaussian(shape, 90, seed, sc).astype(np.float32)
+    n, d = shape[0], int(np.prod(shape[1:]))
+    flat = torch.zeros(lead + n * (d + pad), dtype=dtype, device="cuda")
+    v = flat[lead:].view(n, d + pad)[:, :d].unflatten(1, shape[1:])
+    v.copy_(torch.from_numpy(x).to("cuda"))
+    return v
+
+
+def dt(name):
+    import torch
+    return torch.bfloat16 if name == "bf16" else torch.float32
+
+
+def lse_of(q, k, bias=None):
+    """fp32 natural-log LSE of the scaled logits, [H, n_q] (torch, from host fp64)."""
+    import torch
+    qh, kh = host(q), host(k)
+    out = np.full((qh.shape[1], qh.shape[0]), -np.inf)
+    for h in range(qh.shape[1]):
+        s = qh[:, h] @ kh[:, h].T / np.sqrt(qh.shape[2])
+        if bias is not None:
+            s = s + bias[h]
+        with np.errstate(divide="ignore"):
+            m = s.max(1)
+            out[h] = np.where(np.isneginf(m), -np.inf, np.log(np.exp(s - np.where(np.isneginf(m), 0, m)[:, None]).sum(1)) + m)
+    return torch.from_numpy(out.astype(np.float32)).to("cuda").contiguous()
+
+
+# ------------------------------------------------------------------------------------------ mass
+def check_mass(q, k, ll, lh, mass, decay, bias=None, **kw):
+    import torch
+    from kv_cache_compression_tma_b200 import ispa
+    n_k = k.shape[0]
+    want = orc.attn_mass(host(q), host(k), host(ll), None if lh is None else host(lh), host(mass)[:, :n_k], decay,
+                         None if bias is None else host(bias)[:, :n_k])
+    tail = mass[:, n_k:].clone()
+    ispa.attn_mass(q, k, ll, lh, mass, kv_bias=bias, decay=decay, **kw)
+    assert ispa.get_device_status() == ispa.ISPA_OK
+    got = host(mass)[:, :n_k]
+    assert np.array_equal(got[want == 0], want[want == 0])
+    nz = want != 0
+    assert np.max(np.abs(got[nz] - want[nz]) / np.abs(want[nz]), initial=0.0) <= MASS_TOL
+    assert torch.equal(mass[:, n_k:], tail)
+
+
+@pytest.mark.parametrize("dtype,hd,n_q,n_k,H", [
+    ("bf16", 128, 1, 1, 1), ("bf16", 128, 1, 1000, 3), ("bf16", 64, 3, 257, 2), ("bf16", 128, 17, 129, 2),
+    ("bf16", 128, 128, 256, 2), ("bf16", 64, 129, 255, 2), ("bf16", 128, 300, 700, 2), ("bf16", 64, 513, 130, 1),
+    ("fp32", 16, 5, 70, 3), ("fp32", 32, 64, 96, 2), ("fp32", 64, 33, 31, 2), ("fp32", 128, 2, 300, 2),
+])
+@pytest.mark.parametrize("biased", [False, True])
+def test_mass(cuda_ok, dtype, hd, n_q, n_k, H, biased):
+    import torch
+    q, k = tensor((n_q, H, hd), 1, dt(dtype), 2.0), tensor((n_k, H, hd), 2, dt(dtype))
+    bias = None
+    if biased:
+        b = np.log(1 + np.floor(np.abs(inp.gaussian((H, n_k + 3), 91, 1)) * 2.5).clip(0, 4)).astype(np.float32)
+        b[inp.gaussian((H, n_k + 3), 91, 2) > 1.0] = -np.inf
+        bias = torch.from_numpy(b).cuda()
+    lh = lse_of(q, k, None if bias is None else host(bias)[:, :n_k])
+    ll = lh + 0.5
+    ll[torch.isinf(ll)] = 1.0
+    mass = torch.from_numpy(np.abs(inp.gaussian((H, n_k + 5), 91, 3)).astype(np.float32)).cuda()
+    check_mass(q, k, ll, lh, mass, 0.75, bias)
+
+
+@pytest.mark.parametrize("n_q", [2, 200])
+def test_mass_rows_without_keys_masked_nan_and_decay_zero(cuda_ok, n_q):
+    """Rows with both lse's -inf add nothing; an excluded key's NaN stays out; decay 0 does not read the
+    old mass (NaN there); no history branch; strided and (CUDA cores) unaligned operands."""
+    import torch
+    from kv_cache_compression_tma_b200 import ispa
+    H, hd, n_k = 2, 128, 140
+    q, k = tensor((n_q, H, hd), 3, torch.bfloat16, 2.0, pad=8), tensor((n_k, H, hd), 4, torch.bfloat16, pad=16)
+    bias = torch.zeros((H, n_k + 1), device="cuda")[:, 1:]  # 4-byte aligned only
+    bias[:, 7] = -float("inf")
+    ll = lse_of(q, k, host(bias))
+    k[7] = float("nan")
+    ll[:, n_q // 2] = -float("inf")
+    mass = torch.full((H, n_k), float("nan"), device="cuda")
+    check_mass(q, k, ll, None, mass, 0.0, bias)
+    assert (mass[:, 7] == 0).all()
+    k[7] = 0
+    for lead in (0, 1):
+        qq, kk = tensor((n_q, H, 32), 5, torch.bfloat16, 2.0, 1, lead), tensor((n_k, H, 32), 6, torch.bfloat16, 1.0, 1, lead)
+        check_mass(qq, kk, lse_of(qq, kk), None, mass.fill_(1.0), 1.0, cuda_cores=True)
+    with pytest.raises(ispa.IspaError) as e:
+        ispa.attn_mass(qq, kk, ll, None, mass)
+    assert e.value.status == ispa.ISPA_ERR_UNSUPPORTED
+    with pytest.raises(ValueError):
+        ispa.attn_mass(q, k, ll[:, :1], None, mass)
+    # no queries: the old weights decay, and that is all
+    mass.fill_(3.0)
+    ispa.attn_mass(q[:0], k, ll[:, :0].contiguous(), None, mass, decay=0.5)
+    assert (mass == 1.5).all()
+
+
+# ------------------------------------------------------------------------------------------ insert
+def check_insert(cap, n, n_new, H, hd, dtype, seed, below=0, frm=None, pad=0, lead=0, separate=False, ties=False, mass_new=True):
+    import torch
+    from kv_cache_compression_tma_b200 import ispa
+    k, v = tensor((cap, H, hd), seed, dt(dtype), pad=pad, lead=lead), tensor((cap, H, hd), seed + 1, dt(dtype), pad=pad, lead=lead)
+    kn, vn = tensor((n_new, H, hd), seed + 2, dt(dtype), pad=2 * pad, lead=lead), tensor((n_new, H, hd), seed + 3, dt(dtype), pad=2 * pad, lead=lead)
+    m = inp.gaussian((H, cap + 2), 92, seed).astype(np.float32)
+    mn = inp.gaussian((H, n_new + 1), 92, seed + 1).astype(np.float32)
+    if ties:
+        m, mn = np.round(m), np.round(mn)
+        m[:, ::7], mn[:, ::5] = np.nan, -0.0
+    mass, mass_n = torch.from_numpy(m).cuda(), torch.from_numpy(mn).cuda()[:, :n_new]
+    pos = torch.from_numpy(np.argsort(inp.gaussian((H, cap + 2), 92, seed + 2), axis=1).astype(np.int32)).cuda()
+    pos_new, frm = cap + 2, (2 ** 31 - 1 if frm is None else cap + 2 + n_new - frm)
+    if not mass_new:
+        mn = np.zeros_like(mn)
+        mass_n = None
+    src = orc.cache_insert(m[:, :n], pos.cpu().numpy()[:, :n], mn[:, :n_new], pos_new, cap, below, frm)
+    before = [t.clone() for t in (k, v, mass, pos)]
+    mo, po = (torch.full_like(mass, 9.0), torch.full_like(pos, 9)) if separate else (mass, pos)
+    mo0, po0 = mo.clone(), po.clone()
+    total = ispa.cache_insert(k, v, mass, pos, n, kn, vn, mass_n, pos_new, keep_below=below, keep_from=frm,
+                              mass_out=mo if separate else None, pos_out=po if separate else None)
+    assert total == src.shape[1] == min(cap, n + n_new)
+    at = torch.from_numpy(src).cuda()
+    hh = torch.arange(H, device="cuda")[:, None]
+    for got, old, new in ((k, before[0], kn), (v, before[1], vn)):
+        want = torch.cat([old[:n], new])[at, hh].transpose(0, 1)
+        assert torch.equal(got[:total], want) and torch.equal(got[total:], old[total:])
+    zeros = torch.zeros((H, n_new), device="cuda")
+    want = torch.cat([before[2][:, :n], mass_n if mass_new else zeros], 1).gather(1, at)
+    assert torch.equal(torch.nan_to_num(mo[:, :total], nan=77.0), torch.nan_to_num(want, nan=77.0))
+    news = (pos_new + torch.arange(n_new, device="cuda", dtype=torch.int32)).expand(H, n_new)
+    assert torch.equal(po[:, :total], torch.cat([before[3][:, :n], news], 1).gather(1, at))
+    same = lambda a, b: torch.equal(torch.nan_to_num(a, nan=77.0), torch.nan_to_num(b, nan=77.0))
+    assert same(mo[:, total:], mo0[:, total:]) and torch.equal(po[:, total:], po0[:, total:])
+    if separate:
+        assert same(mass, before[2]) and torch.equal(pos, before[3])
+
+
+@pytest.mark.parametrize("cap,n,n_new,H,hd,dtype", [
+    (1, 1, 1, 1, 16, "fp32"), (1, 0, 3, 2, 64, "bf16"), (8, 0, 5, 2, 64, "bf16"), (100, 100, 1, 3, 128, "bf16"),
+    (100, 97, 10, 3, 128, "bf16"), (64, 64, 200, 2, 64, "bf16"), (1025, 1025, 700, 2, 32, "bf16"),
+    (5000, 5000, 1300, 2, 64, "bf16"), (20000, 19990, 321, 1, 16, "bf16"), (333, 333, 333, 2, 32, "fp32"),
+])
+@pytest.mark.parametrize("separate", [False, True])
+def test_insert(cuda_ok, cap, n, n_new, H, hd, dtype, separate):
+    check_insert(cap, n, n_new, H, hd, dtype, 10, separate=separate)
+
+
+def test_insert_ties_nan_protection_and_layouts(cuda_ok):
+    for cap, n, n_new in ((60, 60, 25), (3000, 2990, 900)):
+        check_insert(cap, n, n_new, 2, 64, "bf16", 20, ties=True)
+        check_insert(cap, n, n_new, 2, 64, "bf16", 21, below=cap // 4, frm=n_new // 2, ties=True, separate=True)
+        check_insert(cap, n, n_new, 2, 64, "bf16", 22, frm=n_new, pad=8)            # every new token protected
+        check_insert(cap, n, n_new, 2, 64, "bf16", 23, below=2 ** 30, pad=3, lead=1)  # everything protected; unaligned rows
+        check_insert(cap, n, n_new, 2, 64, "bf16", 24, mass_new=False)
+
+
+def test_insert_slices_beyond_shared_memory(cuda_ok):
+    """More candidates per CTA than their order keys fit in shared memory."""
+    check_insert(700000, 700000, 90, 1, 16, "bf16", 30, ties=True)
+    check_insert(700000, 699950, 90, 1, 16, "bf16", 31, separate=True)
+
+
+# ------------------------------------------------------------------------------------------ blocks
+@pytest.mark.parametrize("dtype,H,hd,n_k,block,first,pad,lead", [
+    ("bf16", 1, 64, 1, 64, 0, 0, 0), ("bf16", 3, 128, 1000, 128, 0, 8, 0), ("bf16", 2, 64, 640, 64, 7, 0, 0),
+    ("bf16", 2, 128, 200, 96, 1, 1, 1), ("bf16", 5, 16, 77, 5, 0, 0, 0), ("fp32", 2, 32, 95, 32, 0, 4, 0),
+    ("fp32", 3, 16, 50, 7, 3, 1, 1),
+])
+def test_block_means(cuda_ok, dtype, H, hd, n_k, block, first, pad, lead):
+    import torch
+    from kv_cache_compression_tma_b200 import ispa
+    k = tensor((n_k, H, hd), 40, dt(dtype), pad=pad, lead=lead)
+    nb = -(-n_k // block)
+    means = torch.full((nb + 2, H, hd), 5.0, device="cuda")
+    ispa.block_means(k, means, block, first=first)
+    got = means.cpu().numpy()
+    want = orc.block_means(host(k), block)[first:].astype(np.float32)
+    if dtype == "bf16":
+        assert np.array_equal(got[first:nb], want)
+    else:
+        assert np.max(np.abs(got[first:nb] - want) / np.abs(want)) <= 2.0 ** -23
+    assert (got[:first] == 5.0).all() and (got[nb:] == 5.0).all()
+
+
+@pytest.mark.parametrize("dtype,H,hd,n_q,q_block,nb,n_sel", [
+    ("bf16", 1, 64, 1, 1, 1, 1), ("bf16", 3, 128, 1, 1, 1500, 32), ("bf16", 2, 128, 9, 1, 130, 16),
+    ("bf16", 2, 64, 300, 128, 40, 7), ("bf16", 2, 128, 1290, 128, 700, 64), ("bf16", 1, 128, 5, 128, 16384, 300),
+    ("bf16", 2, 64, 10, 4, 5, 9), ("fp32", 2, 32, 64, 32, 3, 2), ("fp32", 2, 16, 50, 7, 33, 33), ("bf16", 2, 64, 3, 1, 0, 4),
+])
+def test_block_select(cuda_ok, dtype, H, hd, n_q, q_block, nb, n_sel):
+    import torch
+    from kv_cache_compression_tma_b200 import ispa
+    q = tensor((n_q, H, hd), 50, dt(dtype), 2.0, pad=3, lead=1)
+    means = tensor((nb, H, hd), 51, torch.float32, 0.1, pad=1)
+    if nb > 8:  # exact ties
+        means[nb // 2:nb // 2 + 3] = means[1]
+    idx = ispa.block_select(q, means, n_sel, q_block=q_block)
+    assert np.array_equal(idx.cpu().numpy(), orc.block_select(host(q), host(means), n_sel, q_block))
+
+
+def test_block_select_all_equal_and_nan(cuda_ok):
+    import torch
+    from kv_cache_compression_tma_b200 import ispa
+    q = torch.ones((2, 1, 64), dtype=torch.bfloat16, device="cuda")
+    means = torch.ones((500, 1, 64), device="cuda")
+    assert ispa.block_select(q, means, 9).cpu().tolist() == [[list(range(9))] * 2]
+    means[:498] = float("nan")
+    assert ispa.block_select(q, means, 4).cpu().tolist() == [[[0, 1, 498, 499]] * 2]
+
+
+# ------------------------------------------------------------------------------------------ sparse attention
+def sparse_case(dtype, H, hd, n_q, q_block, n_sink, n_loc, n_hist, block, n_sel, seed, pad=0, lead=0):
+    import torch
+    names = ("k_sink", "v_sink", "k_loc", "v_loc", "k_hist", "v_hist")
+    sizes = (n_sink, n_sink, n_loc, n_loc, n_hist, n_hist)
+    t = {"q": tensor((n_q, H, hd), seed, dt(dtype), 2.0, pad, lead)}
+    for i, (w, n) in enumerate(zip(names, sizes)):
+        t[w] = tensor((n, H, hd), seed + 1 + i, dt(dtype), 1.0, pad, lead)
+    groups, nb = -(-n_q // q_block), -(-n_hist // block)
+    r = np.random.default_rng(seed)
+    idx = np.full((H, groups, n_sel), -1, np.int32)
+    for h in range(H):
+        for g in range(groups):
+            m = [min(n_sel, nb), 0, r.integers(0, min(n_sel, nb) + 1)][min(2, (h + g) % 4)]
+            idx[h, g, :m] = np.sort(r.permutation(nb)[:m])
+    return t, torch.from_numpy(idx).cuda()
+
+
+def check_sparse(t, idx, block, q_block, tol, **kw):
+    import torch
+    from kv_cache_compression_tma_b200 import ispa
+    out = ispa.block_sparse_attn(*t.values(), idx, block=block, q_block=q_block, **kw)
+    assert ispa.get_device_status() == ispa.ISPA_OK
+    ref = orc.block_sparse(*(host(x) for x in t.values()), idx.cpu().numpy(), block, q_block)
+    n_q = t["q"].shape[0]
+    ol, of = (ref[w].reshape(n_q, -1) for w in ("O_loc", "O_full"))
+    assert rel(host(out["o_loc"]), ol) <= tol["o_loc"]
+    assert rel(host(out["o_full"]), of) <= tol["o_full"]
+    assert rel(host(out["d"]), of - ol) <= tol["d"]
+    assert np.max(np.abs(host(out["lse_loc"]) - ref["lse_loc"])) <= tol["lse_loc"]
+    none = np.isneginf(ref["lse_hist"])
+    got = host(out["lse_hist"])
+    assert np.array_equal(np.isneginf(got), none)
+    assert np.max(np.abs(got[~none] - ref["lse_hist"][~none]), initial=0.0) <= tol["lse_hist"]
+    H = none.shape[0]
+    rows = torch.from_numpy(none.T).cuda()
+    o = [out[w].view(n_q, H, -1) for w in ("o_loc", "o_full", "d")]
+    assert torch.equal(o[0][rows], o[1][rows]) and (o[2][rows] == 0).all()
+    return out
+
+
+@pytest.mark.parametrize("H,hd,n_q,n_sink,n_loc,n_hist,block,n_sel", [
+    (1, 64, 1, 0, 1, 1, 64, 1), (3, 128, 1, 40, 100, 1000, 64, 5), (2, 128, 5, 0, 33, 777, 128, 3),
+    (2, 64, 3, 10, 0, 300, 32, 20), (2, 128, 1, 100, 200, 40000, 128, 200), (1, 128, 2, 5, 5, 50, 7, 4),
+])
+def test_sparse_rows_bf16(cuda_ok, H, hd, n_q, n_sink, n_loc, n_hist, block, n_sel):
+    t, idx = sparse_case("bf16", H, hd, n_q, 1, n_sink, n_loc, n_hist, block, n_sel, 60)
+    check_sparse(t, idx, block, 1, ROW_TOL)
+    t, idx = sparse_case("bf16", H, hd, n_q, 1, n_sink, n_loc, n_hist, block, n_sel, 61, pad=1, lead=1)
+    check_sparse(t, idx, block, 1, ROW_TOL)
+
+
+@pytest.mark.parametrize("H,hd,n_q,q_block,n_sink,n_loc,n_hist,block,n_sel", [
+    (2, 32, 64, 32, 16, 32, 95, 32, 2), (2, 16, 9, 4, 0, 20, 100, 16, 9), (1, 128, 7, 1, 3, 3, 64, 64, 1),
+    (3, 64, 5, 128, 2, 9, 200, 10, 6),
+])
+def test_sparse_rows_fp32(cuda_ok, H, hd, n_q, q_block, n_sink, n_loc, n_hist, block, n_sel):
+    t, idx = sparse_case("fp32", H, hd, n_q, q_block, n_sink, n_loc, n_hist, block, n_sel, 62, pad=4)
+    check_sparse(t, idx, block, q_block, F32_TOL)
+
+
+def test_sparse_odd_lists(cuda_ok):
+    """Lists in any order, with entries that name no block, a block listed twice, n_sel == 0, and NaN in
+    every key and value that no list names."""
+    import torch
+    from kv_cache_compression_tma_b200 import ispa
+    t, _ = sparse_case("bf16", 1, 128, 2, 1, 4, 8, 300, 64, 1, 63)
+    for name in ("k_hist", "v_hist"):
+        t[name][64:128] = float("nan")
+        t[name][192:256] = float("nan")
+    idx = torch.tensor([[[4, -7, 0, 5, 2 ** 31 - 1, 2], [2, 4, 0, -1, 99, -2 ** 31]]], dtype=torch.int32, device="cuda")
+    out = check_sparse(t, idx, 64, 1, ROW_TOL)
+    twice = torch.tensor([[[0, 0], [2, 2]]], dtype=torch.int32, device="cuda")
+    two = check_sparse(t, twice, 64, 1, ROW_TOL)
+    once = check_sparse(t, twice[:, :, :1].contiguous(), 64, 1, ROW_TOL)
+    assert torch.allclose(two["lse_hist"], once["lse_hist"] + np.log(2.0), atol=1e-5)
+    none = check_sparse(t, idx[:, :, :0].contiguous(), 64, 1, ROW_TOL)
+    assert torch.equal(none["o_full"], none["o_loc"]) and torch.equal(none["o_loc"], out["o_loc"])
+    with pytest.raises(ValueError):
+        ispa.block_sparse_attn(*t.values(), idx[:, :1].contiguous(), block=64)
+    with pytest.raises(ispa.IspaError) as e:
+        ispa.block_sparse_attn(*t.values(), idx[:, :1].contiguous(), block=64, q_block=2)
+    assert e.value.status == ispa.ISPA_ERR_UNSUPPORTED
+
+
+# ------------------------------------------------------------------------------------------ together
+def test_streaming_loop_with_eviction_and_block_selection(cuda_ok):
+    """Chunks stream through a MassCache of fixed size: attend, accumulate, insert; then a BlockIndex over
+    the cache selects blocks for sparse attention.  Every step against the oracle on the same state."""
+    import torch
+    from kv_cache_compression_tma_b200 import ispa
+    H, hd, cap, F = 2, 64, 200, 90
+    mc = ispa.MassCache(H, hd, cap)
+    sink = tensor((20, H, hd), 70, torch.bfloat16), tensor((20, H, hd), 71, torch.bfloat16)
+    for step in range(4):
+        s = 72 + 10 * step
+        q, kc, vc = (tensor((F, H, hd), s + i, torch.bfloat16, sc) for i, sc in ((0, 2.0), (1, 1.0), (2, 1.0)))
+        kh, vh = mc.segment()
+        o = ispa.dual_stream_attn(q, *sink, kc, vc, kh, vh)
+        before = host(mc.mass)[:, :mc.n]
+        mc.accumulate(q, o["lse_loc"], o["lse_hist"], decay=0.9)
+        want = orc.attn_mass(host(q), host(kh), host(o["lse_loc"]), host(o["lse_hist"]), before, 0.9)
+        assert np.allclose(host(mc.mass)[:, :mc.n], want, rtol=MASS_TOL, atol=0)
+        m_new = torch.zeros((H, F), device="cuda")
+        ispa.attn_mass(q, kc, o["lse_loc"], o["lse_hist"], m_new, decay=0.0)
+        n, mass, pos, old = mc.n, mc.mass.cpu().numpy(), mc.pos.cpu().numpy(), mc.k.clone()
+        mc.insert(kc, vc, m_new, first=4, recent=10)
+        src = orc.cache_insert(mass[:, :n], pos[:, :n], m_new.cpu().numpy(), step * F, cap, 4, step * F + F - 10)
+        at = torch.from_numpy(src).cuda()
+        want = torch.cat([old[:n], kc])[at, torch.arange(H, device="cuda")[:, None]].transpose(0, 1)
+        assert mc.n == min(cap, (step + 1) * F) and torch.equal(mc.k[:mc.n], want)
+        assert set(range(4)) <= set(mc.pos[0, :mc.n].cpu().tolist())
+    kh, vh = mc.segment()
+    bi = ispa.BlockIndex(H, hd, cap, block=64)
+    bi.extend(kh[:100])
+    bi.extend(kh)
+    assert np.array_equal(bi.means.cpu().numpy(), orc.block_means(host(kh), 64).astype(np.float32))
+    idx = bi.select(q[:1], 2)
+    assert np.array_equal(idx.cpu().numpy(), orc.block_select(host(q[:1]), host(bi.means), 2, 1))
+    t = dict(q=q[:1], ks=sink[0], vs=sink[1], kl=kc, vl=vc, kh=kh, vh=vh)
+    check_sparse(t, idx, 64, 1, ROW_TOL)
+
+
+def test_captured_and_on_another_stream(cuda_ok):
+    """All five calls captured once and replayed on new values in the same buffers, and run eagerly on a
+    side stream: the same bits as eager calls on the current stream."""
+    import torch
+    from kv_cache_compression_tma_b200 import ispa
+    H, hd, cap, n_new = 2, 128, 600, 50
+    q, k, v = tensor((8, H, hd), 80, torch.bfloat16, 2.0), tensor((cap, H, hd), 81, torch.bfloat16), tensor((cap, H, hd), 82, torch.bfloat16)
+    kn, vn = tensor((n_new, H, hd), 83, torch.bfloat16), tensor((n_new, H, hd), 84, torch.bfloat16)
+    mass, pos = torch.rand((H, cap), device="cuda"), torch.arange(cap, dtype=torch.int32, device="cuda").repeat(H, 1)
+    out = {w: torch.zeros((8, H * hd), dtype=torch.bfloat16, device="cuda") for w in ("o_loc", "o_full", "d_out")}
+    out.update({w: torch.zeros((H, 8), device="cuda") for w in ("lse_loc", "lse_hist")})
+    means, idx = torch.zeros((10, H, hd), device="cuda"), torch.zeros((H, 8, 3), dtype=torch.int32, device="cuda")
+    buffers = [k, v, mass, pos, means, idx, *out.values()]
+
+    def step():
+        ispa.block_means(k, means, 64)
+        ispa.block_select(q, means, 3, out=idx)
+        ispa.block_sparse_attn(q, kn, vn, kn, vn, k, v, idx, block=64, **out)
+        ispa.attn_mass(q, k, out["lse_loc"], out["lse_hist"], mass, decay=0.5)
+        ispa.cache_insert(k, v, mass, pos, cap, kn, vn, None, cap, keep_from=cap + 20)
+
+    start = [b.clone() for b in buffers]
+    reset = lambda: [b.copy_(s) for b, s in zip(buffers, start)]
+    step()
+    torch.cuda.synchronize()
+    want = [b.clone() for b in buffers]
+    reset()
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        step()
+    torch.cuda.current_stream().wait_stream(side)
+    assert all(torch.equal(a, b) for a, b in zip(buffers, want))
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step()
+    for _ in range(2):
+        reset()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(buffers, want))
+    assert ispa.get_device_status() == ispa.ISPA_OK
