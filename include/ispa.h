@@ -396,8 +396,8 @@ ISPA_API ispa_status ispa_block_select(int32_t dtype, int32_t n_heads, int32_t h
  *   listed twice counts twice.  A row without any history key gets lse_hist = -inf, O_full = O_loc and
  *   D = 0.  n_sel == 0 (idx unused) is attention over sink and local alone.
  * Every entry of idx is read on the device when the kernel runs.  ISPA_BF16 with q_block a multiple of
- * 128 runs on the tensor cores (block 64 or 128, head_dim 64 or 128 and the alignment rules of
- * ispa_dual_stream_attn, else ISPA_ERR_UNSUPPORTED), ISPA_BF16 with q_block 1 (each query its own
+ * 128 runs on the tensor cores (block 64 or 128, n_sel <= 4096, head_dim 64 or 128 and the alignment rules
+ * of ispa_dual_stream_attn, else ISPA_ERR_UNSUPPORTED), ISPA_BF16 with q_block 1 (each query its own
  * picks: the single-token form) on CUDA cores at any alignment; another q_block is
  * ISPA_ERR_UNSUPPORTED.  ISPA_F32, or ISPA_BF16 with ISPA_ATTN_CUDA_CORES, runs on CUDA cores with any
  * q_block >= 1, block of 1 to 65536, head_dim 16, 32, 64 or 128 and any alignment.

@@ -1,0 +1,523 @@
+// attn_blocks_tc.cu -- dual-stream attention over sink, local and selected history blocks on tcgen05
+// tensor cores: one CTA per (128 query rows, head), whose rows share one list of history blocks.
+//
+// The algorithm is the dense dual-stream kernel's: keys are walked once in tiles of 128, local branch
+// first, an online softmax (m, l, fp32 accumulator in TMEM) per branch, and
+//   O_loc = O_A / l_loc,  O_full = w_loc O_loc + w_hist O_B / l_hist,  D = O_full - O_loc.
+// What differs is where a history tile comes from.  The CTA first turns its list into halves of 64
+// keys (a block is one or two of them; entries that name no block, and empty halves of the history's
+// last block, are dropped), and a history tile is any two consecutive halves: two 64-row TMA boxes per
+// 64 columns instead of one 128-row box.  So both block sizes fill whole MMA tiles, and a ragged block
+// may lie anywhere in the list.  Softmax thread part p of a row owns half p's columns, so each half's
+// count of real keys masks exactly one thread's columns.
+//
+// Warp roles (352 threads): warp 0 Q and the K ring, warp 2 the V ring, warp 1 TMEM and the MMAs
+// (S_t = Q K_t^T into S buffer t%2; O += P_t V_t with P_t read from TMEM), warps 3..10 softmax and
+// epilogue, two threads per row.  Two commits per tile: s_full[t%2] (also frees K_t), o_done[t%2] (also
+// frees V_t).  TMEM columns: [0,256) two S/P buffers, [256,256+HD) O_A, then O_B.
+// Every barrier wait is bounded (sm100.cuh); one that runs out records ISPA_ERR_TIMEOUT and unwinds.
+#include <math.h>
+#include <string.h>
+
+#include "internal.h"
+#include "sm100.cuh"
+
+namespace ispa {
+namespace {
+
+constexpr int kBM = 128;    // query rows per CTA
+constexpr int kBN = 128;    // keys per tile
+constexpr int kHalf = 64;   // keys per half
+constexpr int kFirstSoftmaxWarp = 3;
+constexpr int kSoftmaxThreads = 256;
+constexpr int kThreads = 32 * kFirstSoftmaxWarp + kSoftmaxThreads;
+constexpr int kMaxSel = 4096;             // list entries per row group
+constexpr float kRescaleThreshold = 8.0f;  // log2 units
+
+struct Maps {
+  CUtensorMap q;
+  CUtensorMap k[3];    // sink, local: {64 cols, 128 rows}; history: {64 cols, 64 rows}
+  CUtensorMap v[3];
+  CUtensorMap out[3];  // O_loc, O_full, D
+};
+
+struct Params {
+  int n_q, n_kv[3];
+  int tiles[2];  // sink, local
+  float scale_log2;
+  bool want_d;
+  float* lse_loc;
+  float* lse_hist;
+  unsigned* status;
+  const int32_t* idx;  // [n_heads, groups, n_sel]
+  int n_sel, block, groups, rows_per_group, n_blocks;
+};
+
+template <int HD>
+struct Cfg {
+  static constexpr int kBoxes = HD / 64;
+  static constexpr int kBoxBytes = 128 * 128;  // 64 columns of 128 rows
+  static constexpr int kTileBytes = 128 * HD * 2;
+  static constexpr int kOffQ = 0;
+  static constexpr int kOffK = kOffQ + kTileBytes;
+  static constexpr int kOffV = kOffK + 2 * kTileBytes;
+  static constexpr int kOffBar = kOffV + 2 * kTileBytes;
+  // q_full, k_full[2], v_full[2], s_full[2], p_ready[2], o_done[2], o_final, final
+  static constexpr int kNumBars = 13;
+  static constexpr int kOffMisc = kOffBar + kNumBars * 8 + 8;
+  static constexpr int kOffMax = kOffMisc + 32;             // [3 slots][128 rows] row maxima
+  static constexpr int kOffList = kOffMax + 3 * kBM * 4;    // first key of each half
+  static constexpr uint32_t kIdescQK = idesc_bf16_f32(kBM, kBN, false, false);
+  static constexpr uint32_t kIdescPV = idesc_bf16_f32(kBM, HD, false, true);
+  static_assert(kOffList + 2 * kMaxSel * 4 <= 232448, "shared memory budget");
+};
+
+__device__ __forceinline__ void store_tile_2d(const CUtensorMap* map, const void* smem_src, int32_t x, int32_t y) {
+  asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.tile.bulk_group [%0, {%2, %3}], [%1];" ::"l"(
+                   reinterpret_cast<uint64_t>(map)),
+               "r"(smem_u32(smem_src)), "r"(x), "r"(y)
+               : "memory");
+}
+
+template <int HD>
+__global__ void __launch_bounds__(kThreads, 1) attn_blocks_tc_kernel(const __grid_constant__ Maps maps, const Params p) {
+  using C = Cfg<HD>;
+  extern __shared__ __align__(1024) uint8_t smem[];
+  if ((smem_u32(smem) & 1023) != 0) {  // the swizzled TMA / UMMA layouts need a 1024-byte aligned base
+    if (threadIdx.x == 0) atomicOr(p.status, kStatusInternal);
+    return;
+  }
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::kOffBar);
+  uint64_t* q_full = bars;
+  uint64_t* k_full = bars + 1;
+  uint64_t* v_full = bars + 3;
+  uint64_t* s_full = bars + 5;
+  uint64_t* p_ready = bars + 7;
+  uint64_t* o_done = bars + 9;
+  uint64_t* o_final = bars + 11;
+  uint64_t* final_bar = bars + 12;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::kOffMisc);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::kOffMisc + 4);
+  volatile int* never = reinterpret_cast<volatile int*>(smem + C::kOffMisc + 8);  // stays 0: drain waits
+  int* n_halves_slot = reinterpret_cast<int*>(smem + C::kOffMisc + 12);
+  int* list = reinterpret_cast<int*>(smem + C::kOffList);
+
+  const int warp = threadIdx.x >> 5;
+  const int lane = threadIdx.x & 31;
+  const int head = blockIdx.y;
+  const int q0 = blockIdx.x * kBM;
+
+  if (threadIdx.x == 0) {
+    mbar_init(q_full, 1);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(k_full + i, 1);
+      mbar_init(v_full + i, 1);
+      mbar_init(s_full + i, 1);
+      mbar_init(p_ready + i, kSoftmaxThreads / 32);
+      mbar_init(o_done + i, 1);
+    }
+    mbar_init(o_final, 1);
+    mbar_init(final_bar, 1);
+    *abort_flag = 0;
+    *never = 0;
+    fence_mbar_init();
+  }
+  if (warp == 1) {
+    tmem_alloc(tmem_slot, 512);
+    tmem_relinquish();
+  }
+  if (warp == 2) {  // the list of halves, in list order
+    const int32_t* row = p.idx + (static_cast<int64_t>(head) * p.groups + q0 / p.rows_per_group) * p.n_sel;
+    const int per = p.block / kHalf;
+    int n = 0;
+    for (int i = 0; i < p.n_sel; i += 32) {
+      const int pick = i + lane < p.n_sel ? row[i + lane] : -1;
+      int c = 0, key0 = 0;
+      if (pick >= 0 && pick < p.n_blocks) {
+        key0 = pick * p.block;
+        c = min(per, (p.n_kv[2] - key0 + kHalf - 1) / kHalf);
+      }
+      int inc = c;
+#pragma unroll
+      for (int off = 1; off < 32; off <<= 1) {
+        const int v = __shfl_up_sync(0xffffffffu, inc, off);
+        if (lane >= off) inc += v;
+      }
+      for (int j = 0; j < c; ++j) list[n + inc - c + j] = key0 + j * kHalf;
+      n += __shfl_sync(0xffffffffu, inc, 31);
+    }
+    if (lane == 0) {
+      *n_halves_slot = n;
+      list[n] = p.n_kv[2];  // the missing half of an odd list: past the end, so TMA fills zeros
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  const int n_halves = *n_halves_slot;
+  const int T1 = p.tiles[0] + p.tiles[1];
+  const int T = T1 + (n_halves + 1) / 2;
+
+  if (warp == 0 || warp == 2) {
+    // ------------------------------------------------------------------ TMA producers (K: warp 0, V: warp 2)
+    if (lane == 0) {
+      const bool is_k = warp == 0;
+      uint64_t* full = is_k ? k_full : v_full;
+      uint64_t* empty = is_k ? s_full : o_done;  // stage t % 2 frees with the MMA of tile t - 2
+      if (is_k) {
+        mbar_arrive_expect_tx(q_full, C::kTileBytes);
+#pragma unroll
+        for (int b = 0; b < C::kBoxes; ++b)
+          tma_load_2d(smem + C::kOffQ + b * C::kBoxBytes, &maps.q, q_full, head * HD + 64 * b, q0);
+      }
+      int issued = 0;
+      for (int t = 0; t < T; ++t) {
+        const int s = t & 1;
+        if (t >= 2 && !mbar_wait(empty + s, ((t >> 1) - 1) & 1, abort_flag)) {
+          atomicOr(p.status, kStatusTimeout);
+          *abort_flag = 1;
+          break;
+        }
+        mbar_arrive_expect_tx(full + s, C::kTileBytes);
+        uint8_t* dst = smem + (is_k ? C::kOffK : C::kOffV) + s * C::kTileBytes;
+        if (t < T1) {
+          const int seg = t < p.tiles[0] ? 0 : 1;
+          const int key0 = (t - (seg ? p.tiles[0] : 0)) * kBN;
+          const CUtensorMap* map = is_k ? &maps.k[seg] : &maps.v[seg];
+#pragma unroll
+          for (int b = 0; b < C::kBoxes; ++b) tma_load_2d(dst + b * C::kBoxBytes, map, full + s, head * HD + 64 * b, key0);
+        } else {
+          const CUtensorMap* map = is_k ? &maps.k[2] : &maps.v[2];
+          const int key0 = list[2 * (t - T1)], key1 = list[2 * (t - T1) + 1];
+#pragma unroll
+          for (int b = 0; b < C::kBoxes; ++b) {
+            tma_load_2d(dst + b * C::kBoxBytes, map, full + s, head * HD + 64 * b, key0);
+            tma_load_2d(dst + b * C::kBoxBytes + kHalf * 128, map, full + s, head * HD + 64 * b, key1);
+          }
+        }
+        issued = t + 1;
+      }
+      // Never leave the CTA with bulk copies in flight: wait for the last load of every stage.
+      if (*abort_flag) {
+        for (int t = issued - 1; t >= 0 && t >= issued - 2; --t) mbar_wait(full + (t & 1), (t >> 1) & 1, never);
+        if (is_k) mbar_wait(q_full, 0, never);
+      }
+    }
+  } else if (warp == 1) {
+    // ------------------------------------------------------------------ MMA issuer
+    if (lane == 0) {
+      bool ok = mbar_wait(q_full, 0, abort_flag);
+      tc_fence_after();
+      const uint32_t q_base = smem_u32(smem + C::kOffQ);
+      auto issue_pv = [&](int u) -> bool {
+        const int b = u & 1;
+        if (!mbar_wait(p_ready + b, (u >> 1) & 1, abort_flag)) return false;
+        if (!mbar_wait(v_full + b, (u >> 1) & 1, abort_flag)) return false;
+        tc_fence_after();
+        const uint32_t o_tmem = tmem + 256 + (u >= T1 ? HD : 0);
+        const bool first = (u == 0) || (u == T1);
+        const uint32_t v_base = smem_u32(smem + C::kOffV + b * C::kTileBytes);
+#pragma unroll
+        for (int kk = 0; kk < kBN / 16; ++kk)
+          umma_ts(o_tmem, tmem + b * 128 + kk * 8, sw128_desc(v_base + kk * 16 * 128, C::kBoxBytes, 1024), C::kIdescPV,
+                  (!first || kk > 0) ? 1u : 0u);
+        umma_commit(o_done + b);
+        return true;
+      };
+      for (int t = 0; ok && t < T; ++t) {
+        const int s = t & 1;
+        if (!mbar_wait(k_full + s, (t >> 1) & 1, abort_flag)) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        const uint32_t k_base = smem_u32(smem + C::kOffK + s * C::kTileBytes);
+#pragma unroll
+        for (int kk = 0; kk < HD / 16; ++kk) {
+          const uint32_t off = (kk >> 2) * C::kBoxBytes + (kk & 3) * 32;
+          umma_ss(tmem + s * 128, sw128_desc(q_base + off, 16, 1024), sw128_desc(k_base + off, 16, 1024), C::kIdescQK,
+                  kk > 0 ? 1u : 0u);
+        }
+        umma_commit(s_full + s);
+        if (t > 0 && !issue_pv(t - 1)) {
+          ok = false;
+          break;
+        }
+      }
+      if (ok && T > 0) ok = issue_pv(T - 1);
+      if (!ok) {
+        atomicOr(p.status, kStatusTimeout);
+        *abort_flag = 1;
+      }
+      umma_commit(o_final);
+      umma_commit(final_bar);
+      mbar_wait(final_bar, 0, never);  // every MMA this thread issued has completed before TMEM is released
+    }
+  } else {
+    // ------------------------------------------------------------------ softmax + epilogue
+    const int quarter = warp & 3;                      // TMEM lane quarter this warp may access
+    const int part = (warp - kFirstSoftmaxWarp) >> 2;  // 64 key columns of S (HD/2 columns of O)
+    const int row = quarter * 32 + lane;               // query row within the tile == TMEM lane
+    const uint32_t lane_addr = static_cast<uint32_t>(quarter * 32) << 16;
+    // Row maxima of the key tiles: slot t % 3 collects tile t's maximum over the row's two threads by a
+    // shared-memory atomic max on order-preserving integer images; part 0 clears the slot of tile t-1
+    // after the barrier of tile t, ready for t+2.
+    int* mslot = reinterpret_cast<int*>(smem + C::kOffMax);
+    auto ordered = [](int i) { return i >= 0 ? i : i ^ 0x7fffffff; };  // an involution
+    const int kNegInf = ordered(__float_as_int(-INFINITY));
+    const int bar_id = 1 + quarter;  // named barrier of this row quarter's two warps
+    const float sl2 = p.scale_log2;
+    constexpr int kCols = kBN / 2;   // S columns per thread: one half
+    constexpr int kOCols = HD / 2;   // O columns per thread
+    float m = -INFINITY, l = 0.f;    // l: partial row sum over this thread's columns
+    float m_loc = -INFINITY, l_loc = 0.f;
+    // A warp whose bounded wait ran out stops working but keeps executing one barrier per tile.
+    bool alive = true;
+    if (part == 0)
+#pragma unroll
+      for (int i = 0; i < 3; ++i) mslot[i * kBM + row] = kNegInf;
+    asm volatile("bar.sync %0, 64;" ::"r"(bar_id) : "memory");
+    uint32_t r[kCols];
+    for (int t = 0; t < T; ++t) {
+      const int b = t & 1;
+      int lim;  // how many of this thread's columns hold real keys
+      if (t < T1) {
+        const int seg = t < p.tiles[0] ? 0 : 1;
+        lim = p.n_kv[seg] - (t - (seg ? p.tiles[0] : 0)) * kBN - part * kCols;
+      } else {
+        lim = p.n_kv[2] - list[2 * (t - T1) + part];
+      }
+      if (t == T1) {  // branch switch: freeze the local branch, start the history branch
+        m_loc = m;
+        l_loc = l;
+        m = -INFINITY;
+        l = 0.f;
+      }
+      const bool first = (t == 0) || (t == T1);
+      if (alive) alive = mbar_wait_warp(s_full + b, (t >> 1) & 1, abort_flag);
+      const uint32_t s_addr = tmem + lane_addr + b * 128;
+      float mx = -INFINITY;
+      if (alive) {
+        tc_fence_after();
+#pragma unroll
+        for (int c = 0; c < kCols / 32; ++c) tmem_ld32(s_addr + part * kCols + c * 32, r + c * 32);
+        tmem_wait_ld();
+        if (lim >= kCols) {
+          float m8[kCols / 8];
+#pragma unroll
+          for (int i = 0; i < kCols / 8; ++i) {
+            const float* v = reinterpret_cast<const float*>(r + 8 * i);
+            m8[i] = max3f(max3f(v[0], v[1], v[2]), max3f(v[3], v[4], v[5]), fmaxf(v[6], v[7]));
+          }
+          mx = max3f(max3f(m8[0], m8[1], m8[2]), max3f(m8[3], m8[4], m8[5]), fmaxf(m8[6], m8[7]));
+        } else {
+#pragma unroll
+          for (int j = 0; j < kCols; ++j) {
+            const float x = j < lim ? __uint_as_float(r[j]) : -INFINITY;
+            r[j] = __float_as_uint(x);
+            mx = fmaxf(mx, x);
+          }
+        }
+      }
+      const int slot = (t % 3) * kBM + row;
+      atomicMax(mslot + slot, ordered(__float_as_int(mx)));
+      asm volatile("bar.sync %0, 64;" ::"r"(bar_id) : "memory");
+      mx = __int_as_float(ordered(mslot[slot])) * sl2;
+      if (part == 0) mslot[((t + 2) % 3) * kBM + row] = kNegInf;
+      if (!alive) continue;
+      bool rescale = false;
+      float alpha = 1.f;
+      if (first) {
+        m = mx;
+      } else if (mx > m + kRescaleThreshold) {
+        alpha = fast_exp2(m - mx);
+        m = mx;
+        rescale = true;
+      }
+      const uint64_t sl2x2 = pack_f2(sl2, sl2), negm2 = pack_f2(-m, -m);
+      uint64_t acc[4] = {0ull, 0ull, 0ull, 0ull};
+      uint32_t pk[kCols / 2];
+#pragma unroll
+      for (int j = 0; j < kCols; j += 2) {
+        const uint64_t y = fma_f2(pack_f2(__uint_as_float(r[j]), __uint_as_float(r[j + 1])), sl2x2, negm2);
+        float y0, y1;
+        unpack_f2(y, y0, y1);
+        const float p0 = fast_exp2(y0), p1 = fast_exp2(y1);
+        acc[(j >> 1) & 3] = add_f2(acc[(j >> 1) & 3], pack_f2(p0, p1));
+        pk[j >> 1] = pack_bf16x2(p0, p1);
+      }
+      float a0, a1, a2, a3, a4, a5, a6, a7;
+      unpack_f2(acc[0], a0, a1);
+      unpack_f2(acc[1], a2, a3);
+      unpack_f2(acc[2], a4, a5);
+      unpack_f2(acc[3], a6, a7);
+      l = l * alpha + (((a0 + a1) + (a2 + a3)) + ((a4 + a5) + (a6 + a7)));
+      tmem_st32(s_addr + part * (kCols / 2), pk);
+      // The warp rescales together if any of its rows needs it; only then must PV_{t-1} be complete.
+      // S_t complete implies PV_{t-2} complete, so the parity wait on o_done[(t-1) % 2] cannot alias.
+      const bool any = __any_sync(0xffffffffu, rescale);
+      if (any && t > 0) alive = mbar_wait_warp(o_done + ((t - 1) & 1), ((t - 1) >> 1) & 1, abort_flag);
+      if (!alive) continue;
+      if (any) {
+        tc_fence_after();
+        const uint32_t o_addr = tmem + lane_addr + 256 + (t >= T1 ? HD : 0) + part * kOCols;
+#pragma unroll
+        for (int c = 0; c < kOCols / 32; ++c) {
+          uint32_t o[32];
+          tmem_ld32(o_addr + c * 32, o);
+          tmem_wait_ld();
+#pragma unroll
+          for (int j = 0; j < 32; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * alpha);
+          tmem_st32(o_addr + c * 32, o);
+        }
+      }
+      tmem_wait_st();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(p_ready + b);
+    }
+    if (alive) alive = mbar_wait_warp(o_final, 0, abort_flag);
+    // Partial row sums exchanged through the K ring: o_final has seen every MMA complete, and every load
+    // the MMAs waited for, so no copy or MMA touches the ring any more.
+    float* xchg = reinterpret_cast<float*>(smem + C::kOffK);
+    const bool has_hist = n_halves > 0;
+    if (!has_hist) {
+      m_loc = m;
+      l_loc = l;
+    }
+    xchg[part * kBM + row] = l_loc;
+    xchg[(2 + part) * kBM + row] = l;
+    asm volatile("bar.sync %0, 64;" ::"r"(bar_id) : "memory");
+    const float l_loc_row = xchg[row] + xchg[kBM + row], l_hist_row = xchg[2 * kBM + row] + xchg[3 * kBM + row];
+    // staging tile of output w (0 O_loc, 1 O_full, 2 D) in the idle rings
+    auto stage = [&](int w) -> uint8_t* {
+      return w < 2 ? smem + C::kOffV + w * C::kTileBytes : smem + C::kOffK + C::kTileBytes;
+    };
+    if (!alive) {
+      atomicOr(p.status, kStatusTimeout);
+      *abort_flag = 1;
+    } else {
+      tc_fence_after();
+      const float lse_loc2 = m_loc + __log2f(l_loc_row);
+      const float lse_hist2 = has_hist ? m + __log2f(l_hist_row) : -INFINITY;
+      float w_loc = 1.f, w_hist = 0.f;
+      if (has_hist) {
+        const float mm = fmaxf(lse_loc2, lse_hist2);
+        const float a = exp2f(lse_loc2 - mm), bb = exp2f(lse_hist2 - mm);
+        w_loc = a / (a + bb);
+        w_hist = bb / (a + bb);
+      }
+      const float inv_l_loc = 1.f / l_loc_row;
+      const float inv_l_hist = has_hist ? 1.f / l_hist_row : 0.f;
+      const uint32_t oa_addr = tmem + lane_addr + 256 + part * kOCols;
+      auto put = [&](int which, int col, const float* v8) {  // 8 values at tile column col, 128-byte swizzle
+        uint4 w;
+        w.x = pack_bf16x2(v8[0], v8[1]);
+        w.y = pack_bf16x2(v8[2], v8[3]);
+        w.z = pack_bf16x2(v8[4], v8[5]);
+        w.w = pack_bf16x2(v8[6], v8[7]);
+        *reinterpret_cast<uint4*>(stage(which) + (col >> 6) * C::kBoxBytes + row * 128 + ((((col & 63) >> 3) ^ (row & 7)) << 4)) = w;
+      };
+#pragma unroll 1
+      for (int c = 0; c < kOCols / 32; ++c) {
+        uint32_t oa[32], ob[32];
+        tmem_ld32(oa_addr + c * 32, oa);
+        if (has_hist) tmem_ld32(oa_addr + HD + c * 32, ob);
+        tmem_wait_ld();
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          float vl[8], vf[8], vd[8];
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            vl[j] = __uint_as_float(oa[8 * i + j]) * inv_l_loc;
+            vf[j] = has_hist ? fmaf(w_loc, vl[j], w_hist * (__uint_as_float(ob[8 * i + j]) * inv_l_hist)) : vl[j];
+            vd[j] = vf[j] - vl[j];
+          }
+          const int col = part * kOCols + c * 32 + 8 * i;
+          put(0, col, vl);
+          put(1, col, vf);
+          if (p.want_d) put(2, col, vd);
+        }
+      }
+      if (q0 + row < p.n_q && part == 0) {
+        const float ln2 = 0.69314718055994531f;
+        const int64_t at = static_cast<int64_t>(head) * p.n_q + q0 + row;
+        p.lse_loc[at] = lse_loc2 * ln2;
+        p.lse_hist[at] = has_hist ? lse_hist2 * ln2 : -INFINITY;
+      }
+      asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+    }
+    // every softmax thread has staged its part (or the CTA gave up); one thread stores the tiles
+    asm volatile("bar.sync 5, %0;" ::"n"(kSoftmaxThreads) : "memory");
+    if (warp == kFirstSoftmaxWarp && lane == 0 && !*abort_flag) {
+      for (int w = 0; w < (p.want_d ? 3 : 2); ++w)
+        for (int b = 0; b < C::kBoxes; ++b) store_tile_2d(&maps.out[w], stage(w) + b * C::kBoxBytes, head * HD + 64 * b, q0);
+      asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+      asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    __syncwarp();
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+template <int HD>
+cudaError_t launch_hd(const AttnLaunch& a, const BlockList& b, cudaStream_t stream, int* n_launched) {
+  using C = Cfg<HD>;
+  Maps maps;
+  memset(&maps, 0, sizeof(maps));
+  const uint64_t d = static_cast<uint64_t>(a.n_heads) * HD;
+  bool ok = make_map_bf16_2d(&maps.q, a.q, a.n_q, d, a.ld_q, 64, kBM);
+  Params p;
+  memset(&p, 0, sizeof(p));
+  for (int s = 0; s < 3; ++s) {
+    p.n_kv[s] = static_cast<int>(a.n_kv[s]);
+    if (a.n_kv[s] == 0) continue;
+    if (s < 2) p.tiles[s] = (p.n_kv[s] + kBN - 1) / kBN;
+    const uint32_t box = s == 2 ? kHalf : kBN;
+    ok = ok && make_map_bf16_2d(&maps.k[s], a.k[s], a.n_kv[s], d, a.ld_k[s], 64, box) &&
+         make_map_bf16_2d(&maps.v[s], a.v[s], a.n_kv[s], d, a.ld_v[s], 64, box);
+  }
+  ok = ok && make_map_bf16_2d(&maps.out[0], a.o_loc, a.n_q, d, a.ld_o, 64, kBM) &&
+       make_map_bf16_2d(&maps.out[1], a.o_full, a.n_q, d, a.ld_o, 64, kBM) &&
+       (!a.d_out || make_map_bf16_2d(&maps.out[2], a.d_out, a.n_q, d, a.ld_o, 64, kBM));
+  if (!ok) return cudaErrorInvalidValue;
+  p.n_q = static_cast<int>(a.n_q);
+  p.scale_log2 = a.scale * 1.4426950408889634f;
+  p.want_d = a.d_out != nullptr;
+  p.lse_loc = a.lse_loc;
+  p.lse_hist = a.lse_hist;
+  p.status = a.status;
+  p.idx = b.idx;
+  p.n_sel = a.n_kv[2] > 0 ? b.n_sel : 0;
+  p.block = b.block;
+  p.groups = static_cast<int>(b.groups);
+  p.rows_per_group = b.q_block;
+  p.n_blocks = b.n_blocks;
+  cudaError_t e = cudaFuncSetAttribute(attn_blocks_tc_kernel<HD>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                       C::kOffList + 2 * kMaxSel * 4 + 16);
+  if (e != cudaSuccess) return e;
+  // the list holds one or two halves per entry, and one entry past an odd count
+  const int smem = C::kOffList + (p.n_sel * (b.block / kHalf) + 1) * 4;
+  dim3 grid(static_cast<unsigned>((a.n_q + kBM - 1) / kBM), static_cast<unsigned>(a.n_heads));
+  attn_blocks_tc_kernel<HD><<<grid, kThreads, smem, stream>>>(maps, p);
+  *n_launched += 1;
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+bool attn_blocks_tc_supported(const AttnLaunch& a, const BlockList& b) {
+  return attn_tc_supported(a) && (b.block == 64 || b.block == 128) && b.q_block % kBM == 0 && b.n_sel <= kMaxSel;
+}
+
+cudaError_t launch_attn_blocks_tc(const AttnLaunch& a, const BlockList& b, cudaStream_t s, int* n_launched) {
+  return a.head_dim == 128 ? launch_hd<128>(a, b, s, n_launched) : launch_hd<64>(a, b, s, n_launched);
+}
+
+}  // namespace ispa

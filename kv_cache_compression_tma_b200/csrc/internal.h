@@ -177,6 +177,9 @@ struct BlockList {
   int64_t groups;      // ceil(n_q / q_block)
   int n_blocks;        // ceil(n_kv[history] / block)
 };
+// tcgen05 kernel: bf16, attn_tc_supported's rules, block 64 or 128, q_block a multiple of 128
+bool attn_blocks_tc_supported(const AttnLaunch& a, const BlockList& b);
+cudaError_t launch_attn_blocks_tc(const AttnLaunch& a, const BlockList& b, cudaStream_t s, int* n_launched);
 // one row and head per cluster, CUDA cores (either dtype, any head_dim of the API, any alignment)
 cudaError_t launch_attn_blocks_rows(const AttnLaunch& a, const BlockList& b, cudaStream_t s, int* n_launched);
 

@@ -522,14 +522,17 @@ ispa_status ispa_block_sparse_attn(const ispa_attn_args* a, const int32_t* idx, 
   if (n_sel > 0 && (!idx || !aligned(idx, 4))) return ISPA_ERR_INVALID_ARG;
   if (biased) return ISPA_ERR_UNSUPPORTED;
   const bool cuda_cores = (a->flags & ISPA_ATTN_CUDA_CORES) != 0 || a->dtype == ISPA_F32;
-  if (!cuda_cores && q_block != 1) return ISPA_ERR_UNSUPPORTED;
-  if (a->n_q == 0) return ISPA_OK;
   const BlockList B{idx, n_sel, block, q_block, (a->n_q + q_block - 1) / q_block,
                     static_cast<int>((a->n_kv[ISPA_SEG_HIST] + block - 1) / block)};
+  // bf16 groups of rows run on the tensor cores or not at all, unless the caller asks for CUDA cores
+  const bool rows = cuda_cores || q_block == 1;
+  if (!rows && !attn_blocks_tc_supported(L, B)) return ISPA_ERR_UNSUPPORTED;
+  if (a->n_q == 0) return ISPA_OK;
   L.status = status_ptr();
   if (!L.status) return ISPA_ERR_CUDA;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
   int n = 0;
-  cudaError_t e = launch_attn_blocks_rows(L, B, static_cast<cudaStream_t>(stream), &n);
+  cudaError_t e = rows ? launch_attn_blocks_rows(L, B, st, &n) : launch_attn_blocks_tc(L, B, st, &n);
   count(n);
   return e == cudaSuccess ? ISPA_OK : ISPA_ERR_CUDA;
 }

@@ -297,6 +297,39 @@ def test_sparse_rows_fp32(cuda_ok, H, hd, n_q, q_block, n_sink, n_loc, n_hist, b
     check_sparse(t, idx, block, q_block, F32_TOL)
 
 
+@pytest.mark.parametrize("H,hd,n_q,q_block,n_sink,n_loc,n_hist,block,n_sel", [
+    (1, 64, 1, 128, 0, 1, 1, 64, 1), (2, 128, 300, 128, 40, 300, 1000, 64, 5), (2, 128, 257, 128, 0, 130, 777, 128, 3),
+    (2, 64, 128, 128, 10, 0, 300, 64, 9), (1, 128, 700, 256, 128, 256, 4000, 128, 33), (3, 64, 130, 384, 1, 1, 63, 128, 2),
+    (1, 128, 129, 128, 0, 64, 192, 128, 2),
+])
+@pytest.mark.parametrize("pad", [0, 8])
+def test_sparse_tensor_cores(cuda_ok, H, hd, n_q, q_block, n_sink, n_loc, n_hist, block, n_sel, pad):
+    t, idx = sparse_case("bf16", H, hd, n_q, q_block, n_sink, n_loc, n_hist, block, n_sel, 64, pad=pad)
+    check_sparse(t, idx, block, q_block, ATTN_TOL)
+
+
+def test_sparse_tensor_cores_odd_lists_and_dense_limit(cuda_ok):
+    """Any order, entries that name no block, a ragged block in the middle of the list, NaN in the blocks
+    that no list names; and every block listed = the dense kernel's result within its tolerance."""
+    import torch
+    from kv_cache_compression_tma_b200 import ispa
+    for block in (64, 128):
+        t, _ = sparse_case("bf16", 1, 128, 200, 128, 4, 8, 5 * block - 20, block, 1, 65)
+        every = torch.arange(5, dtype=torch.int32, device="cuda").repeat(1, 2, 1)
+        a = check_sparse(t, every, block, 128, ATTN_TOL)
+        d = ispa.dual_stream_attn(*t.values())
+        assert rel(host(a["o_full"]), host(d["o_full"])) <= ATTN_TOL["o_full"]
+        for name in ("k_hist", "v_hist"):
+            t[name][block:2 * block] = float("nan")
+        idx = torch.tensor([[[4, -7, 0, 5, 2 ** 31 - 1, 2, 3], [2, 4, 0, -1, 99, -2 ** 31, 2]]], dtype=torch.int32, device="cuda")
+        check_sparse(t, idx, block, 128, ATTN_TOL)
+        none = check_sparse(t, idx[:, :, :0].contiguous(), block, 128, ATTN_TOL)
+        assert torch.equal(none["o_full"], none["o_loc"])
+        with pytest.raises(ispa.IspaError) as e:
+            ispa.block_sparse_attn(*t.values(), idx[:, :, :1].contiguous(), block=96, q_block=128)
+        assert e.value.status == ispa.ISPA_ERR_UNSUPPORTED
+
+
 def test_sparse_odd_lists(cuda_ok):
     """Lists in any order, with entries that name no block, a block listed twice, n_sel == 0, and NaN in
     every key and value that no list names."""
