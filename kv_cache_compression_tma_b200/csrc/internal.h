@@ -227,6 +227,10 @@ struct MassLaunch {
   int64_t ld_mass;        // of both
   unsigned* status;
 };
+// tcgen05 kernel: bf16, head_dim 64 or 128, TMA-compatible strides, at least one query
+bool mass_tc_supported(const MassLaunch& a);
+cudaError_t launch_mass_tc(const MassLaunch& a, cudaStream_t s, int* n_launched);
+// CUDA cores, any case
 cudaError_t launch_mass_rows(const MassLaunch& a, cudaStream_t s, int* n_launched);
 
 // ------------------------------------------------------------------ cache insertion with eviction

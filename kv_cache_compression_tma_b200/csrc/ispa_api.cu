@@ -47,6 +47,9 @@ void count(int n) { g_launches.fetch_add(static_cast<uint64_t>(n)); }
 
 bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
 
+// Up to this many queries the row kernel of ispa_attn_mass reads the keys at the memory's rate.
+constexpr int64_t kMassRowsMaxQueries = 8;
+
 // head dimensions of the kernels that spread a head's row over lanes
 bool rows_head_dim(int32_t hd) { return hd == 16 || hd == 32 || hd == 64 || hd == 128; }
 
@@ -434,8 +437,10 @@ ispa_status ispa_attn_mass(int32_t dtype, int32_t n_heads, int32_t head_dim, con
                softmax_scale > 0.f ? softmax_scale : 1.0f / sqrtf(static_cast<float>(head_dim)), decay, mass, mass_out,
                ld_mass, status_ptr()};
   if (!L.status) return ISPA_ERR_CUDA;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
   int n = 0;
-  cudaError_t e = launch_mass_rows(L, static_cast<cudaStream_t>(stream), &n);
+  const bool tc = !cuda_cores && n_q > kMassRowsMaxQueries && mass_tc_supported(L);
+  cudaError_t e = tc ? launch_mass_tc(L, st, &n) : launch_mass_rows(L, st, &n);
   count(n);
   return e == cudaSuccess ? ISPA_OK : ISPA_ERR_CUDA;
 }

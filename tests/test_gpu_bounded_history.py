@@ -92,6 +92,28 @@ def test_mass(cuda_ok, dtype, hd, n_q, n_k, H, biased):
     check_mass(q, k, ll, lh, mass, 0.75, bias)
 
 
+@pytest.mark.parametrize("H,n_q,n_k,hd", [(3, 130, 128 * 151 + 5, 64), (1, 8192 + 130, 300, 128), (2, 16640, 140, 64)])
+def test_mass_many_tiles_and_query_chunks(cuda_ok, H, n_q, n_k, hd):
+    """More key tiles than SMs (ranges of a CTA that cross heads, single tiles among pairs) and more
+    queries than one chunk, against a 64-bit product on the GPU."""
+    import torch
+    from kv_cache_compression_tma_b200 import ispa
+    q, k = tensor((n_q, H, hd), 7, torch.bfloat16, 2.0), tensor((n_k, H, hd), 8, torch.bfloat16)
+    ll, lh = (3.0 + torch.rand((H, n_q), device="cuda") for _ in range(2))
+    ll[:, 5] = lh[:, 5] = -float("inf")
+    mass = torch.rand((H, n_k), device="cuda")
+    want = 0.5 * mass.double()
+    live = torch.isfinite(ll[0])
+    for h in range(H):
+        for i in range(0, n_q, 2048):
+            s = q[i:i + 2048, h].double() @ k[:, h].double().T / np.sqrt(hd)
+            w = torch.exp(s - torch.logaddexp(ll[h, i:i + 2048].double(), lh[h, i:i + 2048].double())[:, None])
+            want[h] += w[live[i:i + 2048]].sum(0)
+    ispa.attn_mass(q, k, ll, lh, mass, decay=0.5)
+    assert ispa.get_device_status() == ispa.ISPA_OK
+    assert ((mass.double() - want).abs() / want).max().item() <= MASS_TOL
+
+
 @pytest.mark.parametrize("n_q", [2, 200])
 def test_mass_rows_without_keys_masked_nan_and_decay_zero(cuda_ok, n_q):
     """Rows with both lse's -inf add nothing; an excluded key's NaN stays out; decay 0 does not read the
