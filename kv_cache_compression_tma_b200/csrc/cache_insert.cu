@@ -25,19 +25,24 @@ namespace cg = cooperative_groups;
 namespace ispa {
 namespace {
 
-constexpr int kThreads = 512;
+constexpr int kThreads = 1024;
 constexpr int kWarps = kThreads / 32;
 constexpr int kMaxCluster = 16;
-constexpr int kMaxCached = 40960;  // order keys per CTA held in shared memory (160 KB)
+constexpr int kMaxCached = 32768;   // order keys per CTA held in shared memory (128 KB)
 constexpr int kMaxNewSlice = 4096;  // new tokens per CTA: their list of slots and of sources (32 KB)
+constexpr int kUnroll = 4;          // state words in flight per thread while the keys are formed
 
 struct Shared {
-  uint32_t hist[4][256];        // one histogram per radix pass, so one cluster barrier per pass is enough
+  // Digit counts of one pass, one column per lane: keys of a cache share few leading digits, and lanes
+  // of a warp that add to one address would take turns.
+  uint32_t hist[256][32];
+  uint32_t total[4][256];       // ... summed, one array per pass, so one cluster barrier per pass is enough
   uint32_t sum[kWarps];         // scan scratch
-  uint32_t digit, below;        // the pass's digit and the candidates below it
+  uint32_t digit, below, same;  // the pass's digit, the candidates below it, the candidates in it
   uint32_t counts[4];           // this CTA's {less, equal} of the held slice, then of the new slice
   uint32_t warp_counts[kWarps][4];
-  uint32_t base[4];             // equal / evicted ranks before this CTA: held equal, new equal, holes, survivors
+  uint32_t base[4];             // ranks before this CTA: held equal, new equal, holes, survivors
+  uint32_t holes;               // evicted held entries of the head
   uint32_t first_survivor[kMaxCluster + 1];
 };
 
@@ -47,16 +52,6 @@ __device__ __forceinline__ uint32_t order_key(float mass, int32_t pos, int32_t k
   if (pos < keep_below || pos >= keep_from) mass = INFINITY;
   const uint32_t u = __float_as_uint(mass + 0.f);  // -0 becomes +0
   return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
-}
-
-__device__ __forceinline__ void copy_row(const uint8_t* src, uint8_t* dst, int bytes, int unit, int lane, int lanes) {
-  if (unit == 16) {
-    for (int b = lane * 16; b < bytes; b += lanes * 16)
-      *reinterpret_cast<uint4*>(dst + b) = __ldg(reinterpret_cast<const uint4*>(src + b));
-  } else {
-    for (int b = lane * 2; b < bytes; b += lanes * 2)
-      *reinterpret_cast<uint16_t*>(dst + b) = __ldg(reinterpret_cast<const uint16_t*>(src + b));
-  }
 }
 
 __global__ void __launch_bounds__(kThreads) cache_insert_kernel(const InsertLaunch a, int cached, int unit) {
@@ -91,27 +86,58 @@ __global__ void __launch_bounds__(kThreads) cache_insert_kernel(const InsertLaun
 
   const int total = min(a.capacity, a.n + a.n_new);
   const uint32_t drop = static_cast<uint32_t>(a.n + a.n_new - total);
-  uint32_t threshold = 0;   // candidates below it leave; of those equal to it the last `leave_equal`
-  uint32_t stay_equal = 0;  // ... and the first `stay_equal` stay
+  uint32_t threshold = 0;   // candidates below it leave; of those equal to it
+  uint32_t stay_equal = 0;  // the first `stay_equal` stay
 
+  // Order keys; a state that goes to other arrays is copied on the way (slots of entries that leave are
+  // overwritten by the survivors further below).
+  const bool copy_mass = a.mass_out != a.mass, copy_pos = a.pos_out != a.pos;
+  if ((drop > 0 && cached) || copy_mass || copy_pos) {
+    for (int i0 = tid; i0 < old_n; i0 += kUnroll * kThreads) {
+      float m[kUnroll];
+      int32_t q[kUnroll];
+#pragma unroll
+      for (int u = 0; u < kUnroll; ++u) {
+        const int i = i0 + u * kThreads;
+        m[u] = i < old_n ? mass[old0 + i] : 0.f;
+        q[u] = i < old_n ? pos[old0 + i] : 0;
+      }
+#pragma unroll
+      for (int u = 0; u < kUnroll; ++u) {
+        const int i = i0 + u * kThreads;
+        if (i >= old_n) break;
+        if (cached) keys[i] = order_key(m[u], q[u], a.keep_below, a.keep_from);
+        if (copy_mass) mass_out[old0 + i] = m[u];
+        if (copy_pos) pos_out[old0 + i] = q[u];
+      }
+    }
+  }
   if (drop > 0) {
-    for (int i = tid; i < 4 * 256; i += kThreads) (&sh.hist[0][0])[i] = 0;
     if (cached)
-      for (int i = tid; i < all; i += kThreads) keys[i] = make_key(i);
-    __syncthreads();
+      for (int i = old_n + tid; i < all; i += kThreads) keys[i] = make_key(i);
     uint32_t prefix = 0, left = drop;  // left: how many of the candidates that share the prefix leave
     uint32_t same = 0;                 // candidates that share the prefix after the last pass
     for (int pass = 0; pass < 4; ++pass) {
       const int shift = 24 - 8 * pass;
+      for (int i = tid; i < 256 * 32; i += kThreads) (&sh.hist[0][0])[i] = 0;
+      __syncthreads();
       for (int i = tid; i < all; i += kThreads) {
         const uint32_t k = key_at(i);
-        if (pass == 0 || (k >> (shift + 8)) == (prefix >> (shift + 8))) atomicAdd(&sh.hist[pass][(k >> shift) & 255], 1u);
+        if (pass == 0 || (k >> (shift + 8)) == (prefix >> (shift + 8))) atomicAdd(&sh.hist[(k >> shift) & 255][lane], 1u);
+      }
+      __syncthreads();
+#pragma unroll
+      for (int d = 0; d < 256 / kWarps; ++d) {
+        const uint32_t c = __reduce_add_sync(0xffffffffu, sh.hist[warp * (256 / kWarps) + d][lane]);
+        if (lane == 0) sh.total[pass][warp * (256 / kWarps) + d] = c;
       }
       cluster.sync();
       // every CTA forms the same cluster-wide counts: thread d < 256 holds digit d
       uint32_t c = 0;
-      if (tid < 256)
-        for (int r = 0; r < C; ++r) c += cluster.map_shared_rank(&sh.hist[pass][0], r)[tid];
+      if (tid < 256) {
+#pragma unroll 4
+        for (int r = 0; r < C; ++r) c += cluster.map_shared_rank(&sh.total[pass][0], r)[tid];
+      }
       uint32_t inc = c;
 #pragma unroll
       for (int off = 1; off < 32; off <<= 1) {
@@ -120,20 +146,19 @@ __global__ void __launch_bounds__(kThreads) cache_insert_kernel(const InsertLaun
       }
       if (lane == 31) sh.sum[warp] = inc;
       __syncthreads();
-      uint32_t before = 0;
-      for (int w = 0; w < warp; ++w) before += sh.sum[w];
-      inc += before;
-      // the digit in which the last leaving candidate lies: below < left <= below + c
-      if (tid < 256 && inc - c < left && left <= inc) {
-        sh.digit = static_cast<uint32_t>(tid);
-        sh.below = inc - c;
-        sh.counts[0] = c;
+      if (tid < 256) {
+        for (int w = 0; w < warp; ++w) inc += sh.sum[w];
+        // the digit in which the last leaving candidate lies: below < left <= below + c
+        if (inc - c < left && left <= inc) {
+          sh.digit = static_cast<uint32_t>(tid);
+          sh.below = inc - c;
+          sh.same = c;
+        }
       }
       __syncthreads();
       prefix |= sh.digit << shift;
       left -= sh.below;
-      same = sh.counts[0];
-      __syncthreads();
+      same = sh.same;
     }
     threshold = prefix;
     stay_equal = same - left;
@@ -171,42 +196,47 @@ __global__ void __launch_bounds__(kThreads) cache_insert_kernel(const InsertLaun
     sh.counts[tid] = c;
   }
   cluster.sync();
-  // Ranks before this CTA.  Equal candidates count in candidate order: all held slices, then all new.
-  if (tid == 0) {
-    uint32_t eq = 0, holes = 0, total_old_eq = 0;
-    for (int r = 0; r < C; ++r) total_old_eq += cluster.map_shared_rank(&sh.counts[0], r)[1];
-    uint32_t neq = total_old_eq, surv = 0;
-    auto leaving = [&](uint32_t first, uint32_t n) {  // of n equal candidates from equal-rank `first` on
-      const uint32_t end = first + n;
-      return end > stay_equal ? end - max(first, stay_equal) : 0u;
-    };
-    for (int r = 0; r < C; ++r) {
-      const uint32_t* cc = cluster.map_shared_rank(&sh.counts[0], r);
-      if (r == rank) {
-        sh.base[0] = eq;
-        sh.base[1] = neq;
-        sh.base[2] = holes;
-        sh.base[3] = surv;
-      }
-      sh.first_survivor[r] = surv;
-      const int rn = max(0, min(a.n_new, (r + 1) * new_per) - min(a.n_new, r * new_per));
-      holes += cc[0] + leaving(eq, cc[1]);
-      surv += static_cast<uint32_t>(rn) - cc[2] - leaving(neq, cc[3]);
-      eq += cc[1];
-      neq += cc[3];
-    }
-    sh.first_survivor[C] = surv;
-    sh.digit = holes;  // evicted held entries of the head
-  }
-  __syncthreads();
-  const uint32_t n_holes = sh.digit;
-
-  // Ranks before this warp.
-  uint32_t eq_o = sh.base[0], eq_n = sh.base[1], hole = sh.base[2], surv = 0;
-  auto leaving = [&](uint32_t first, uint32_t n) {
+  // Ranks before this CTA (lane r of warp 0: CTA r).  Equal candidates count in candidate order: all
+  // held slices, then all new ones.
+  auto leaving = [&](uint32_t first, uint32_t n) {  // of n equal candidates from equal-rank `first` on
     const uint32_t end = first + n;
     return end > stay_equal ? end - max(first, stay_equal) : 0u;
   };
+  if (warp == 0) {
+    uint32_t cc[4] = {};
+    if (lane < C)
+#pragma unroll
+      for (int x = 0; x < 4; ++x) cc[x] = cluster.map_shared_rank(&sh.counts[0], lane)[x];
+    auto before = [&](uint32_t v) {  // sum over the CTAs before lane's
+      uint32_t inc = v;
+#pragma unroll
+      for (int off = 1; off < 32; off <<= 1) {
+        const uint32_t w = __shfl_up_sync(0xffffffffu, inc, off);
+        if (lane >= off) inc += w;
+      }
+      return inc - v;
+    };
+    const uint32_t eq = before(cc[1]);
+    const uint32_t neq = before(cc[3]) + __reduce_add_sync(0xffffffffu, cc[1]);
+    const int rn = lane < C ? max(0, min(a.n_new, (lane + 1) * new_per) - min(a.n_new, lane * new_per)) : 0;
+    const uint32_t h = cc[0] + leaving(eq, cc[1]);
+    const uint32_t v = static_cast<uint32_t>(rn) - cc[2] - leaving(neq, cc[3]);
+    const uint32_t hole = before(h), surv = before(v);
+    if (lane == rank) {
+      sh.base[0] = eq;
+      sh.base[1] = neq;
+      sh.base[2] = hole;
+      sh.base[3] = surv;
+    }
+    if (lane <= C) sh.first_survivor[lane] = surv;  // lane C: all of them
+    const uint32_t all_holes = __reduce_add_sync(0xffffffffu, h);
+    if (lane == 0) sh.holes = all_holes;
+  }
+  __syncthreads();
+  const uint32_t n_holes = sh.holes;
+
+  // Ranks before this warp.
+  uint32_t eq_o = sh.base[0], eq_n = sh.base[1], hole = sh.base[2], surv = 0;
   for (int w = 0; w < warp; ++w) {
     hole += sh.warp_counts[w][0] + leaving(eq_o, sh.warp_counts[w][1]);
     eq_o += sh.warp_counts[w][1];
@@ -249,13 +279,7 @@ __global__ void __launch_bounds__(kThreads) cache_insert_kernel(const InsertLaun
     surv += __popc(stay_mask);
     eq_n += __popc(eq_mask);
   }
-  cluster.sync();  // every slot list is complete, and every read of mass and pos above is done
-
-  if (a.mass_out != a.mass)
-    for (int i = tid; i < old_n; i += kThreads) mass_out[old0 + i] = mass[old0 + i];
-  if (a.pos_out != a.pos)
-    for (int i = tid; i < old_n; i += kThreads) pos_out[old0 + i] = pos[old0 + i];
-  if (a.mass_out != a.mass || a.pos_out != a.pos) cluster.sync();  // the survivors overwrite their slots
+  cluster.sync();  // every slot list is complete, every read of mass and pos above done, the copies made
 
   const int mine = static_cast<int>(sh.first_survivor[rank + 1] - sh.first_survivor[rank]);
   for (int i = tid; i < mine; i += kThreads) {
@@ -263,14 +287,30 @@ __global__ void __launch_bounds__(kThreads) cache_insert_kernel(const InsertLaun
     mass_out[slot] = mass_new ? mass_new[t] : 0.f;
     pos_out[slot] = a.pos_new + t;
   }
-  // K by the lower half of each warp, V by the upper half
-  const int half = lane >> 4;
-  const uint8_t* src = static_cast<const uint8_t*>(half ? a.v_new : a.k_new);
-  uint8_t* dst = static_cast<uint8_t*>(half ? a.v : a.k);
+  // K by the lower half of each warp, V by the upper half, kRows tokens in flight
+  constexpr int kRows = 4;
+  const int half = lane >> 4, hl = lane & 15;
   const int64_t col = static_cast<int64_t>(head) * a.row_bytes;
-  for (int i = warp; i < mine; i += kWarps)
-    copy_row(src + static_cast<int64_t>(source_of[i]) * a.ld_new_bytes + col,
-             dst + static_cast<int64_t>(slot_of[i]) * a.ld_cache_bytes + col, a.row_bytes, unit, lane & 15, 16);
+  const uint8_t* src = static_cast<const uint8_t*>(half ? a.v_new : a.k_new) + col;
+  uint8_t* dst = static_cast<uint8_t*>(half ? a.v : a.k) + col;
+  for (int i = warp * kRows; i < mine; i += kWarps * kRows) {
+    if (unit == 16) {
+      for (int b = hl * 16; b < a.row_bytes; b += 256) {
+        uint4 w[kRows];
+#pragma unroll
+        for (int r = 0; r < kRows; ++r)
+          if (i + r < mine) w[r] = __ldg(reinterpret_cast<const uint4*>(src + source_of[i + r] * a.ld_new_bytes + b));
+#pragma unroll
+        for (int r = 0; r < kRows; ++r)
+          if (i + r < mine) *reinterpret_cast<uint4*>(dst + slot_of[i + r] * a.ld_cache_bytes + b) = w[r];
+      }
+    } else {
+      for (int r = 0; r < kRows && i + r < mine; ++r)
+        for (int b = hl * 2; b < a.row_bytes; b += 32)
+          *reinterpret_cast<uint16_t*>(dst + slot_of[i + r] * a.ld_cache_bytes + b) =
+              __ldg(reinterpret_cast<const uint16_t*>(src + source_of[i + r] * a.ld_new_bytes + b));
+    }
+  }
 }
 
 }  // namespace
@@ -280,11 +320,11 @@ bool cache_insert_supported(int64_t n, int64_t n_new) {
 }
 
 cudaError_t launch_cache_insert(const InsertLaunch& a, cudaStream_t s, int* n_launched) {
-  // Cluster size: enough CTAs that a slice is about a thousand candidates, at most 16.
+  // Cluster size: one CTA forms and searches about 16 thousand order keys as fast as a cluster barrier
+  // per pass costs, so a head is split only beyond that.
   const int64_t cand = static_cast<int64_t>(a.n) + a.n_new;
   int C = 1;
-  while (C < kMaxCluster && cand > 1024ll * C) C *= 2;
-  while (C < kMaxCluster && (a.n_new + C - 1) / C > kMaxNewSlice) C *= 2;
+  while (C < kMaxCluster && (cand > 16384ll * C || (a.n_new + C - 1) / C > kMaxNewSlice)) C *= 2;
   const int old_per = (a.n + C - 1) / C, new_per = (a.n_new + C - 1) / C;
   const int cached = old_per + new_per <= kMaxCached;
   const size_t smem = 4ull * ((cached ? old_per + new_per : 0) + 2ll * new_per);

@@ -131,8 +131,9 @@ def _check(status: int, what: str):
 
 def _stream(stream=None) -> int:
     import torch
-    s = torch.cuda.current_stream() if stream is None else stream
-    return int(s.cuda_stream)
+    if stream is None:  # the raw handle: a Stream object costs several microseconds per call
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+    return int(stream.cuda_stream)
 
 
 def _dtype_code(t) -> int:
@@ -150,7 +151,7 @@ def _on_current_device(*tensors):
     import torch
     cur = torch.cuda.current_device()
     for t in tensors:
-        if t is not None and (t.device.type != "cuda" or t.device.index != cur):
+        if t is not None and t.get_device() != cur:  # -1 for a host tensor
             raise ValueError(f"tensor on {t.device}, but the current CUDA device is cuda:{cur}; "
                              f"call under `with torch.cuda.device(...)`")
 
