@@ -30,19 +30,20 @@ constexpr int kWarps = kThreads / 32;
 constexpr int kMaxCluster = 16;
 constexpr int kMaxCached = 32768;   // order keys per CTA held in shared memory (128 KB)
 constexpr int kMaxNewSlice = 4096;  // new tokens per CTA: their list of slots and of sources (32 KB)
-constexpr int kUnroll = 4;          // state words in flight per thread while the keys are formed
+constexpr int kUnroll = 16;         // state words in flight per thread while the keys are formed
+constexpr int kShort = 2048;        // candidates sharing the first digit that are listed apart
 
 struct Shared {
-  // Digit counts of one pass, one column per lane: keys of a cache share few leading digits, and lanes
-  // of a warp that add to one address would take turns.
+  // Counts of the first digit, one column per lane: the keys of a cache share few leading digits, and
+  // lanes of a warp that add to one address would take turns.
   uint32_t hist[256][32];
-  uint32_t total[4][256];       // ... summed, one array per pass, so one cluster barrier per pass is enough
-  uint32_t sum[kWarps];         // scan scratch
-  uint32_t digit, below, same;  // the pass's digit, the candidates below it, the candidates in it
-  uint32_t counts[4];           // this CTA's {less, equal} of the held slice, then of the new slice
-  uint32_t warp_counts[kWarps][4];
-  uint32_t base[4];             // ranks before this CTA: held equal, new equal, holes, survivors
-  uint32_t holes;               // evicted held entries of the head
+  uint32_t total[4][256];             // the CTA's counts, one array per pass: one cluster barrier per pass
+  alignas(16) uint32_t cluster_total[256];
+  uint32_t shortlist[kShort];         // candidates that share the first digit, when they fit
+  uint32_t n_short, digit, below;
+  alignas(16) uint32_t counts[4];     // the CTA's {less, equal} of the held slice, then of the new slice
+  alignas(16) uint32_t all_counts[kMaxCluster][4];  // every CTA's
+  uint32_t warp_counts[kWarps][4];    // the same per warp, then the sum over the warps before
   uint32_t first_survivor[kMaxCluster + 1];
 };
 
@@ -54,8 +55,19 @@ __device__ __forceinline__ uint32_t order_key(float mass, int32_t pos, int32_t k
   return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
 }
 
+// Sum of v over the lanes before this one.
+__device__ __forceinline__ uint32_t warp_before(uint32_t v, int lane) {
+  uint32_t inc = v;
+#pragma unroll
+  for (int off = 1; off < 32; off <<= 1) {
+    const uint32_t w = __shfl_up_sync(0xffffffffu, inc, off);
+    if (lane >= off) inc += w;
+  }
+  return inc - v;
+}
+
 __global__ void __launch_bounds__(kThreads) cache_insert_kernel(const InsertLaunch a, int cached, int unit) {
-  extern __shared__ uint32_t dyn[];
+  extern __shared__ __align__(16) uint32_t dyn[];
   __shared__ Shared sh;
   cg::cluster_group cluster = cg::this_cluster();
   const int C = static_cast<int>(cluster.num_blocks());
@@ -73,7 +85,7 @@ __global__ void __launch_bounds__(kThreads) cache_insert_kernel(const InsertLaun
   const float* mass_new = a.mass_new ? a.mass_new + static_cast<int64_t>(head) * a.ld_new_state : nullptr;
   float* mass_out = a.mass_out + static_cast<int64_t>(head) * a.ld_out;
   int32_t* pos_out = a.pos_out + static_cast<int64_t>(head) * a.ld_out;
-  uint32_t* keys = dyn;                              // [old_n + new_n] when cached
+  uint32_t* keys = dyn;                              // [old_n + new_n] when cached (16-byte aligned)
   int32_t* slot_of = reinterpret_cast<int32_t*>(dyn + (cached ? old_per + new_per : 0));  // [new_per] by survivor rank
   int32_t* source_of = slot_of + new_per;            // [new_per] new token of each survivor
 
@@ -83,6 +95,16 @@ __global__ void __launch_bounds__(kThreads) cache_insert_kernel(const InsertLaun
     return order_key(mass_new ? mass_new[t] : 0.f, a.pos_new + t, a.keep_below, a.keep_from);
   };
   auto key_at = [&](int i) -> uint32_t { return cached ? keys[i] : make_key(i); };
+  // Four consecutive candidates of the held slice from i (a multiple of 4) on, as `none` past the slice.
+  auto four_keys = [&](int i, uint32_t none, uint32_t* k) {
+    if (cached && i + 3 < old_n) {
+      const uint4 w = *reinterpret_cast<const uint4*>(keys + i);
+      k[0] = w.x, k[1] = w.y, k[2] = w.z, k[3] = w.w;
+    } else {
+#pragma unroll
+      for (int x = 0; x < 4; ++x) k[x] = i + x < old_n ? key_at(i + x) : none;
+    }
+  };
 
   const int total = min(a.capacity, a.n + a.n_new);
   const uint32_t drop = static_cast<uint32_t>(a.n + a.n_new - total);
@@ -115,66 +137,99 @@ __global__ void __launch_bounds__(kThreads) cache_insert_kernel(const InsertLaun
   if (drop > 0) {
     if (cached)
       for (int i = old_n + tid; i < all; i += kThreads) keys[i] = make_key(i);
-    uint32_t prefix = 0, left = drop;  // left: how many of the candidates that share the prefix leave
-    uint32_t same = 0;                 // candidates that share the prefix after the last pass
+    for (int i = tid; i < 256 * 32; i += kThreads) (&sh.hist[0][0])[i] = 0;
+    if (tid < 256) sh.total[1][tid] = sh.total[2][tid] = sh.total[3][tid] = 0;
+    if (tid == 0) sh.n_short = 0;
+    __syncthreads();
+#pragma unroll 4
+    for (int i = tid; i < all; i += kThreads) atomicAdd(&sh.hist[key_at(i) >> 24][lane], 1u);
+    __syncthreads();
+#pragma unroll
+    for (int d = 0; d < 256 / kWarps; ++d) {
+      const uint32_t c = __reduce_add_sync(0xffffffffu, sh.hist[warp * (256 / kWarps) + d][lane]);
+      if (lane == 0) sh.total[0][warp * (256 / kWarps) + d] = c;
+    }
+    uint32_t left = drop;  // how many of the candidates that share the digits so far leave
+    bool listed = false;
     for (int pass = 0; pass < 4; ++pass) {
       const int shift = 24 - 8 * pass;
-      for (int i = tid; i < 256 * 32; i += kThreads) (&sh.hist[0][0])[i] = 0;
-      __syncthreads();
-      for (int i = tid; i < all; i += kThreads) {
-        const uint32_t k = key_at(i);
-        if (pass == 0 || (k >> (shift + 8)) == (prefix >> (shift + 8))) atomicAdd(&sh.hist[(k >> shift) & 255][lane], 1u);
+      if (pass > 0) {
+        const int n = listed ? static_cast<int>(sh.n_short) : all;
+        for (int i = tid; i < n; i += kThreads) {
+          const uint32_t k = listed ? sh.shortlist[i] : key_at(i);
+          if ((k >> (shift + 8)) == (threshold >> (shift + 8))) atomicAdd(&sh.total[pass][(k >> shift) & 255], 1u);
+        }
       }
-      __syncthreads();
-#pragma unroll
-      for (int d = 0; d < 256 / kWarps; ++d) {
-        const uint32_t c = __reduce_add_sync(0xffffffffu, sh.hist[warp * (256 / kWarps) + d][lane]);
-        if (lane == 0) sh.total[pass][warp * (256 / kWarps) + d] = c;
-      }
-      cluster.sync();
-      // every CTA forms the same cluster-wide counts: thread d < 256 holds digit d
-      uint32_t c = 0;
-      if (tid < 256) {
+      const uint32_t* counts = sh.total[pass];
+      if (C > 1) {  // every CTA forms the same cluster-wide counts
+        cluster.sync();
+        if (tid < 256) {
+          uint32_t c = 0;
 #pragma unroll 4
-        for (int r = 0; r < C; ++r) c += cluster.map_shared_rank(&sh.total[pass][0], r)[tid];
+          for (int r = 0; r < C; ++r) c += cluster.map_shared_rank(&sh.total[pass][0], r)[tid];
+          sh.cluster_total[tid] = c;
+        }
+        counts = sh.cluster_total;
       }
-      uint32_t inc = c;
-#pragma unroll
-      for (int off = 1; off < 32; off <<= 1) {
-        const uint32_t v = __shfl_up_sync(0xffffffffu, inc, off);
-        if (lane >= off) inc += v;
-      }
-      if (lane == 31) sh.sum[warp] = inc;
       __syncthreads();
-      if (tid < 256) {
-        for (int w = 0; w < warp; ++w) inc += sh.sum[w];
-        // the digit in which the last leaving candidate lies: below < left <= below + c
-        if (inc - c < left && left <= inc) {
-          sh.digit = static_cast<uint32_t>(tid);
-          sh.below = inc - c;
-          sh.same = c;
+      if (warp == 0) {  // the digit of the last leaving candidate: below < left <= below + count; eight a lane
+        const uint4 lo = *reinterpret_cast<const uint4*>(counts + lane * 8), hi = *reinterpret_cast<const uint4*>(counts + lane * 8 + 4);
+        const uint32_t c[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
+        uint32_t sum = 0;
+#pragma unroll
+        for (int d = 0; d < 8; ++d) sum += c[d];
+        uint32_t below = warp_before(sum, lane);
+        if (below < left && left <= below + sum) {  // one lane
+          int d = 0;
+#pragma unroll
+          for (int e = 0; e < 7; ++e)
+            if (d == e && left > below + c[e]) {
+              below += c[e];
+              ++d;
+            }
+          sh.digit = static_cast<uint32_t>(lane * 8 + d);
+          sh.below = below;
         }
       }
       __syncthreads();
-      prefix |= sh.digit << shift;
+      const uint32_t digit = sh.digit, same = counts[digit];
+      threshold |= digit << shift;
       left -= sh.below;
-      same = sh.same;
+      stay_equal = same - left;
+      if (left == same) {  // all of the digit leaves: the threshold is the next digit's start (some candidate stays, so there is one)
+        threshold += 1u << shift;
+        stay_equal = 0xffffffffu;
+        break;
+      }
+      if (pass == 0) {
+        listed = sh.total[0][digit] <= kShort;  // this CTA's own count
+        if (listed) {
+#pragma unroll 4
+          for (int i = tid; i < all; i += kThreads) {
+            const uint32_t k = key_at(i);
+            if ((k >> 24) == digit) sh.shortlist[atomicAdd(&sh.n_short, 1u)] = k;
+          }
+        }
+      }
+      __syncthreads();
     }
-    threshold = prefix;
-    stay_equal = same - left;
   }
 
   // Counts of candidates below and at the threshold: per warp over contiguous pieces, so that ranks
   // follow the candidate order.
-  const int old_w = (old_n + kWarps - 1) / kWarps, new_w = (new_n + kWarps - 1) / kWarps;
+  const int old_w = (old_n + 128 * kWarps - 1) / (128 * kWarps) * 128, new_w = (new_n + kWarps - 1) / kWarps;
   const int oa = min(old_n, warp * old_w), ob = min(old_n, oa + old_w);
   const int na = old_n + min(new_n, warp * new_w), nb = min(all, na + new_w);
   if (drop > 0) {
     uint32_t c[4] = {};
-    for (int i = oa + lane; i < ob; i += 32) {
-      const uint32_t k = key_at(i);
-      c[0] += k < threshold;
-      c[1] += k == threshold;
+    for (int i = oa + 4 * lane; i < ob; i += 128) {
+      uint32_t k[4];
+      four_keys(i, 0xffffffffu, k);  // no key is all ones (NaN ranks as -inf)
+#pragma unroll
+      for (int x = 0; x < 4; ++x) {
+        c[0] += k[x] < threshold;
+        c[1] += k[x] == threshold;
+      }
     }
     for (int i = na + lane; i < nb; i += 32) {
       const uint32_t k = key_at(i);
@@ -190,77 +245,76 @@ __global__ void __launch_bounds__(kThreads) cache_insert_kernel(const InsertLaun
     sh.warp_counts[warp][lane] = 0;
   }
   __syncthreads();
-  if (tid < 4) {
-    uint32_t c = 0;
-    for (int w = 0; w < kWarps; ++w) c += sh.warp_counts[w][tid];
-    sh.counts[tid] = c;
+  if (warp == 0) {  // sums over the warps before, and over all of them (kWarps == 32: lane = warp)
+#pragma unroll
+    for (int x = 0; x < 4; ++x) {
+      const uint32_t v = sh.warp_counts[lane][x], before = warp_before(v, lane);
+      sh.warp_counts[lane][x] = before;
+      if (lane == 31) sh.counts[x] = before + v;
+    }
   }
   cluster.sync();
-  // Ranks before this CTA (lane r of warp 0: CTA r).  Equal candidates count in candidate order: all
-  // held slices, then all new ones.
-  auto leaving = [&](uint32_t first, uint32_t n) {  // of n equal candidates from equal-rank `first` on
-    const uint32_t end = first + n;
-    return end > stay_equal ? end - max(first, stay_equal) : 0u;
-  };
-  if (warp == 0) {
+  if (tid < C)
+    *reinterpret_cast<uint4*>(sh.all_counts[tid]) = *reinterpret_cast<const uint4*>(cluster.map_shared_rank(&sh.counts[0], tid));
+  __syncthreads();
+  // Ranks before this warp.  Equal candidates count in candidate order: all held slices, then all new
+  // ones.  Lane r looks at CTA r.
+  auto leaving = [&](uint32_t n) { return n > stay_equal ? n - stay_equal : 0u; };  // of the first n equal ones
+  uint32_t eq_o, eq_n, hole, surv, first, n_holes;
+  {
     uint32_t cc[4] = {};
     if (lane < C)
 #pragma unroll
-      for (int x = 0; x < 4; ++x) cc[x] = cluster.map_shared_rank(&sh.counts[0], lane)[x];
-    auto before = [&](uint32_t v) {  // sum over the CTAs before lane's
-      uint32_t inc = v;
-#pragma unroll
-      for (int off = 1; off < 32; off <<= 1) {
-        const uint32_t w = __shfl_up_sync(0xffffffffu, inc, off);
-        if (lane >= off) inc += w;
-      }
-      return inc - v;
-    };
-    const uint32_t eq = before(cc[1]);
-    const uint32_t neq = before(cc[3]) + __reduce_add_sync(0xffffffffu, cc[1]);
-    const int rn = lane < C ? max(0, min(a.n_new, (lane + 1) * new_per) - min(a.n_new, lane * new_per)) : 0;
-    const uint32_t h = cc[0] + leaving(eq, cc[1]);
-    const uint32_t v = static_cast<uint32_t>(rn) - cc[2] - leaving(neq, cc[3]);
-    const uint32_t hole = before(h), surv = before(v);
-    if (lane == rank) {
-      sh.base[0] = eq;
-      sh.base[1] = neq;
-      sh.base[2] = hole;
-      sh.base[3] = surv;
-    }
-    if (lane <= C) sh.first_survivor[lane] = surv;  // lane C: all of them
-    const uint32_t all_holes = __reduce_add_sync(0xffffffffu, h);
-    if (lane == 0) sh.holes = all_holes;
+      for (int x = 0; x < 4; ++x) cc[x] = sh.all_counts[lane][x];
+    const uint32_t rn = lane < C ? static_cast<uint32_t>(min(a.n_new, (lane + 1) * new_per) - min(a.n_new, lane * new_per)) : 0u;
+    const uint32_t old_eq = __reduce_add_sync(0xffffffffu, cc[1]);
+    const uint32_t eq = warp_before(cc[1], lane), neq = old_eq + warp_before(cc[3], lane);
+    const uint32_t less = warp_before(cc[0], lane), stayed = warp_before(rn - cc[2], lane);
+    // holes before CTA `lane`, survivors before it (lane C: all)
+    const uint32_t h = less + leaving(eq), v = stayed - (leaving(neq) - leaving(old_eq));
+    if (warp == 0 && lane <= C) sh.first_survivor[lane] = v;
+    n_holes = __reduce_add_sync(0xffffffffu, cc[0]) + leaving(old_eq);
+    const uint32_t* wc = sh.warp_counts[warp];
+    eq_o = __shfl_sync(0xffffffffu, eq, rank) + wc[1];
+    eq_n = __shfl_sync(0xffffffffu, neq, rank) + wc[3];
+    hole = __shfl_sync(0xffffffffu, less, rank) + wc[0] + leaving(eq_o);
+    first = __shfl_sync(0xffffffffu, v, rank);  // the CTA's first survivor
+    surv = static_cast<uint32_t>(na - old_n) - wc[2] - (leaving(eq_n) - leaving(eq_n - wc[3]));
   }
   __syncthreads();
-  const uint32_t n_holes = sh.holes;
-
-  // Ranks before this warp.
-  uint32_t eq_o = sh.base[0], eq_n = sh.base[1], hole = sh.base[2], surv = 0;
-  for (int w = 0; w < warp; ++w) {
-    hole += sh.warp_counts[w][0] + leaving(eq_o, sh.warp_counts[w][1]);
-    eq_o += sh.warp_counts[w][1];
-    const int wn = max(0, min(new_n, (w + 1) * new_w) - min(new_n, w * new_w));
-    surv += static_cast<uint32_t>(wn) - sh.warp_counts[w][2] - leaving(eq_n, sh.warp_counts[w][3]);
-    eq_n += sh.warp_counts[w][3];
-  }
   const uint32_t lt = (1u << lane) - 1u;
   if (drop > 0) {
     // evicted held entries: slot of hole rank r goes to the CTA that owns survivor r
-    for (int i = oa; i < ob; i += 32) {
-      const bool in = i + lane < ob;
-      const uint32_t k = in ? key_at(i + lane) : 0xffffffffu;
-      const uint32_t eq_mask = __ballot_sync(0xffffffffu, in && k == threshold);
-      const bool out = in && (k < threshold || (k == threshold && eq_o + __popc(eq_mask & lt) >= stay_equal));
-      const uint32_t out_mask = __ballot_sync(0xffffffffu, out);
-      if (out) {
-        const uint32_t r = hole + __popc(out_mask & lt);
-        int owner = 0;
-        while (r >= sh.first_survivor[owner + 1]) ++owner;  // r < survivors of the head: one leaves per hole
-        cluster.map_shared_rank(slot_of, owner)[r - sh.first_survivor[owner]] = old0 + i + lane;
+    for (int i = oa; i < ob; i += 128) {  // four consecutive entries a lane
+      uint32_t k[4];
+      four_keys(i + 4 * lane, 0xffffffffu, k);
+      bool out[4], any = false;
+      uint32_t eq = 0;
+#pragma unroll
+      for (int x = 0; x < 4; ++x) {
+        out[x] = k[x] < threshold;
+        eq += k[x] == threshold;
+        any = any || k[x] <= threshold;
       }
-      hole += __popc(out_mask);
-      eq_o += __popc(eq_mask);
+      if (!__any_sync(0xffffffffu, any)) continue;
+      if (__any_sync(0xffffffffu, eq > 0)) {
+        uint32_t e = eq_o + warp_before(eq, lane);
+#pragma unroll
+        for (int x = 0; x < 4; ++x)
+          if (k[x] == threshold) out[x] = e++ >= stay_equal;
+        eq_o += __reduce_add_sync(0xffffffffu, eq);
+      }
+      const uint32_t n_out = out[0] + out[1] + out[2] + out[3];
+      uint32_t r = hole + warp_before(n_out, lane);
+#pragma unroll
+      for (int x = 0; x < 4; ++x)
+        if (out[x]) {
+          int owner = 0;
+          while (r >= sh.first_survivor[owner + 1]) ++owner;  // r < survivors of the head: one leaves per hole
+          cluster.map_shared_rank(slot_of, owner)[r - sh.first_survivor[owner]] = old0 + i + 4 * lane + x;
+          ++r;
+        }
+      hole += __reduce_add_sync(0xffffffffu, n_out);
     }
   }
   // surviving new tokens of this CTA, by rank; ranks past the holes take the unused slots from n on
@@ -273,7 +327,7 @@ __global__ void __launch_bounds__(kThreads) cache_insert_kernel(const InsertLaun
     if (stay) {
       const uint32_t local = surv + __popc(stay_mask & lt);
       source_of[local] = new0 + i - old_n + lane;
-      const uint32_t r = sh.base[3] + local;
+      const uint32_t r = first + local;
       if (r >= n_holes) slot_of[local] = a.n + static_cast<int32_t>(r - n_holes);
     }
     surv += __popc(stay_mask);
@@ -320,11 +374,13 @@ bool cache_insert_supported(int64_t n, int64_t n_new) {
 }
 
 cudaError_t launch_cache_insert(const InsertLaunch& a, cudaStream_t s, int* n_launched) {
-  // Cluster size: one CTA forms and searches about 16 thousand order keys as fast as a cluster barrier
-  // per pass costs, so a head is split only beyond that.
+  // Cluster size: a CTA (one per SM: 1024 threads) forms and searches about 16 thousand order keys in the
+  // time of the cluster barriers, so a head is split only beyond that, and only while all clusters
+  // can run at once (clusters of 16 fit 8 times on the GPU's 8 GPCs of 16 to 20 SMs, of 8 twice as often).
   const int64_t cand = static_cast<int64_t>(a.n) + a.n_new;
   int C = 1;
-  while (C < kMaxCluster && (cand > 16384ll * C || (a.n_new + C - 1) / C > kMaxNewSlice)) C *= 2;
+  while (C < kMaxCluster && cand > 16384ll * C && static_cast<int64_t>(a.n_heads) * 2 * C <= 128) C *= 2;
+  while (C < kMaxCluster && (a.n_new + C - 1) / C > kMaxNewSlice) C *= 2;
   const int old_per = (a.n + C - 1) / C, new_per = (a.n_new + C - 1) / C;
   const int cached = old_per + new_per <= kMaxCached;
   const size_t smem = 4ull * ((cached ? old_per + new_per : 0) + 2ll * new_per);
