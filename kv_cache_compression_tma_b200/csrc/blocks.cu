@@ -8,10 +8,15 @@
 // n_sel blocks of highest score.  Scores are formed in 64 bits: they only rank blocks, and with sums of
 // 128 terms fp32 would let the order of summation decide between blocks whose scores are close; the
 // work is one dot product per (group, block), small next to the attention it prunes.
-// A cluster of C CTAs serves C groups of one head: CTA r pools group r's queries and hands the mean to
-// all, each CTA scores 1/C of the blocks for all groups (the means are read once per cluster), sends
+// A cluster of 8 CTAs serves 8 groups of one head: CTA r pools group r's queries and hands the mean to
+// all, each CTA scores 1/8 of the blocks for all groups (so the means are read once per cluster), sends
 // each score to the CTA that owns the group, and that CTA selects (radix select on 64-bit order keys,
-// ties to the lowest block) and writes the picks in ascending order.
+// ties to the lowest block) and writes the picks in ascending order.  The scores are 8 groups x 8
+// blocks x 4 products per mma.m8n8k4 in fp64.  The means go straight from memory into its fragments: a
+// lane's products may be any quarter of the head_dim, so the four lanes of a row take alternate
+// 16-byte pieces and a load covers whole 64-byte runs.  The mean queries stay in shared memory, which
+// leaves registers for four CTAs per SM: a chunk's clusters then all run at once.  A lone group (a
+// single token) is pooled by every CTA for itself and takes fused multiply-adds, an eighth of the work.
 #include <cooperative_groups.h>
 #include <math.h>
 
@@ -64,8 +69,7 @@ __global__ void __launch_bounds__(kMeanThreads) block_means_kernel(const BlockMe
 // ------------------------------------------------------------------------------------------ select
 constexpr int kSelThreads = 256;
 constexpr int kSelWarps = kSelThreads / 32;
-constexpr int kSelCluster = 8;
-constexpr int kTileBlocks = 32;
+constexpr int kSelCluster = 8;  // CTAs, and groups, per cluster
 constexpr int kMaxBlocks = 16384;  // one 64-bit order key per block in the owner's shared memory
 
 __device__ __forceinline__ uint64_t order_key64(double s) {
@@ -74,71 +78,118 @@ __device__ __forceinline__ uint64_t order_key64(double s) {
   return (u >> 63) ? ~u : (u | (1ull << 63));
 }
 
-// grid: (clusters of C CTAs per head) * C, heads.  kCluster groups per cluster.
-template <typename T, int HD>
-__global__ void __launch_bounds__(kSelThreads) block_select_kernel(const BlockSelectLaunch a) {
-  extern __shared__ uint64_t keys[];  // [n_blocks] of the group this CTA owns
-  __shared__ double qm[kSelCluster][HD];
-  __shared__ double kt[kTileBlocks][HD + 2];
+// D (8 x 8) += A (8 x 4) B (4 x 8) in fp64: lane l holds A[l / 4][l % 4], B[l % 4][l / 4] and
+// D[l / 4][2 (l % 4) + {0, 1}].
+__device__ __forceinline__ void mma_f64(double& d0, double& d1, double a, double b) {
+  asm volatile("mma.sync.aligned.m8n8k4.row.col.f64.f64.f64.f64 {%0, %1}, {%2}, {%3}, {%0, %1};"
+               : "+d"(d0), "+d"(d1)
+               : "d"(a), "d"(b));
+}
+
+// grid: (clusters per head) * 8, heads
+template <typename T, int HD, bool kAligned>
+__global__ void __launch_bounds__(kSelThreads, 4) block_select_kernel(const BlockSelectLaunch a) {
+  constexpr int kQuarter = HD / 4;               // products of a lane per score
+  constexpr int kVec = 16 / static_cast<int>(sizeof(T));
+  constexpr int kColThreads = HD / kVec;
+  constexpr int kRowGroups = kSelThreads / kColThreads;
+  extern __shared__ __align__(16) uint64_t keys[];  // [n_blocks] of the group this CTA owns
+  __shared__ __align__(16) double qm[kSelCluster][HD + 2];  // a row's four lanes read two rows' 128 bytes at a time
+  __shared__ double part[kRowGroups][HD];
   __shared__ uint32_t hist[256];
   __shared__ uint32_t sum[kSelWarps];
-  __shared__ uint32_t found[3];  // digit, keys below it, keys in it
+  __shared__ uint32_t found[3];                  // digit, keys below it, keys in it
   cg::cluster_group cluster = cg::this_cluster();
-  const int C = static_cast<int>(cluster.num_blocks());
   const int rank = static_cast<int>(cluster.block_rank());
   const int head = blockIdx.y;
-  const int64_t g0 = static_cast<int64_t>(blockIdx.x / C) * C;
-  const int n_groups = static_cast<int>(a.groups - g0 < C ? a.groups - g0 : C);
+  const int64_t g0 = static_cast<int64_t>(blockIdx.x / kSelCluster) * kSelCluster;
+  const int n_groups = static_cast<int>(a.groups - g0 < kSelCluster ? a.groups - g0 : kSelCluster);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int nb = a.n_blocks;
-  cluster.sync();  // every CTA of the cluster runs before its shared memory is written from another
 
-  if (rank < n_groups) {  // the group's mean query, in 64 bits
-    const int64_t r0 = (g0 + rank) * a.q_block;
+  const int g_own = n_groups > 1 ? rank : 0;
+  double mean = 0.0;
+  if (g_own < n_groups) {  // the group's mean query, in 64 bits, summed in a fixed order
+    const int64_t r0 = (g0 + g_own) * a.q_block;
     const int rows = static_cast<int>(a.n_q - r0 < a.q_block ? a.n_q - r0 : a.q_block);
-    const T* Q = static_cast<const T*>(a.q) + r0 * a.ld_q + static_cast<int64_t>(head) * HD;
-    constexpr int kParts = kSelThreads / HD;
-    double (*part)[HD + 2] = kt;
-    const int e = tid % HD;
-    double s = 0.0;
-#pragma unroll 8
-    for (int r = tid / HD; r < rows; r += kParts) s += static_cast<double>(static_cast<float>(Q[r * a.ld_q + e]));
-    part[tid / HD][e] = s;
+    const int col = (tid % kColThreads) * kVec, tr = tid / kColThreads;
+    const T* Q = static_cast<const T*>(a.q) + r0 * a.ld_q + static_cast<int64_t>(head) * HD + col;
+    double s[kVec] = {};
+#pragma unroll 4
+    for (int r = tr; r < rows; r += kRowGroups) {
+      float v[kVec];
+      unpack<T>(load_raw<T, kAligned>(Q + r * a.ld_q), v);
+#pragma unroll
+      for (int e = 0; e < kVec; ++e) s[e] += static_cast<double>(v[e]);
+    }
+#pragma unroll
+    for (int e = 0; e < kVec; ++e) part[tr][col + e] = s[e];
     __syncthreads();
     if (tid < HD) {
+      const int used = rows < kRowGroups ? rows : kRowGroups;
       double t = 0.0;
-#pragma unroll
-      for (int p = 0; p < kParts; ++p) t += part[p][tid];
-      t /= rows;
-      for (int r = 0; r < C; ++r) cluster.map_shared_rank(&qm[0][0], r)[rank * HD + tid] = t;
+      for (int p = 0; p < used; ++p) t += part[p][tid];
+      mean = t / rows;
     }
   }
-  cluster.sync();
-
-  // scores of this CTA's share of the blocks: lane = block of a tile, warp = group
-  const int per = (nb + C - 1) / C;
-  const int b0 = min(nb, rank * per), b1 = min(nb, b0 + per);
-  for (int t0 = b0; t0 < b1; t0 += kTileBlocks) {
-    __syncthreads();
-    for (int x = tid; x < kTileBlocks * (HD / 4); x += kSelThreads) {
-      const int j = x / (HD / 4), c = (x % (HD / 4)) * 4;
-      if (t0 + j < b1) {
-        const float* m = a.means + static_cast<int64_t>(t0 + j) * a.ld_means + static_cast<int64_t>(head) * HD + c;
+  cluster.sync();  // every CTA of the cluster runs before its shared memory is written from another
+  if (tid < HD) {
+    if (n_groups == 1)
+      qm[0][tid] = mean;
+    else
 #pragma unroll
-        for (int i = 0; i < 4; ++i) kt[j][c + i] = static_cast<double>(__ldg(m + i));
-      }
-    }
+      for (int r = 0; r < kSelCluster; ++r) cluster.map_shared_rank(&qm[rank][0], r)[tid] = mean;  // 0 where no group is
+  }
+  if (n_groups == 1)
     __syncthreads();
-    if (warp < n_groups && t0 + lane < b1) {
-      double s0 = 0.0, s1 = 0.0;
-#pragma unroll 8
-      for (int e = 0; e < HD; e += 2) {
-        const double2 q = *reinterpret_cast<const double2*>(&qm[warp][e]);
-        const double2 k = *reinterpret_cast<const double2*>(&kt[lane][e]);
-        s0 = fma(q.x, k.x, s0);
-        s1 = fma(q.y, k.y, s1);
+  else
+    cluster.sync();
+
+  // Scores of this CTA's share of the blocks, eight at a time per warp.  Lane l: groups and blocks l / 4,
+  // elements 16 i + 4 (l % 4) + {0..3}.
+  const int sub = lane >> 2, c0 = (lane & 3) * 4;
+  const int per = ((nb + kSelCluster - 1) / kSelCluster + 7) / 8 * 8;
+  const int b0 = min(nb, rank * per), b1 = min(nb, b0 + per);
+  uint64_t* owner = cluster.map_shared_rank(keys, n_groups > 1 ? sub : 0);
+  for (int t = b0 + warp * 8; t < b1; t += kSelWarps * 8) {
+    const int64_t b = min(t + sub, b1 - 1);
+    const float* m = a.means + b * a.ld_means + static_cast<int64_t>(head) * HD + c0;
+    uint4 w[kQuarter / 4];
+#pragma unroll
+    for (int i = 0; i < kQuarter / 4; ++i) w[i] = a.means_aligned ? load_raw<float, true>(m + 16 * i) : load_raw<float, false>(m + 16 * i);
+    double d[2][2] = {};
+    if (n_groups > 1) {
+#pragma unroll
+      for (int i = 0; i < kQuarter / 4; ++i) {
+        float v[4];
+        unpack<float>(w[i], v);
+#pragma unroll
+        for (int e = 0; e < 4; e += 2) {
+          const double2 q = *reinterpret_cast<const double2*>(&qm[sub][16 * i + c0 + e]);
+          mma_f64(d[0][0], d[0][1], q.x, static_cast<double>(v[e]));
+          mma_f64(d[1][0], d[1][1], q.y, static_cast<double>(v[e + 1]));
+        }
       }
-      cluster.map_shared_rank(keys, warp)[t0 + lane] = order_key64(s0 + s1);
+      const int bo = t + 2 * (lane & 3);
+      if (sub < n_groups) {
+        const ulonglong2 k2 = make_ulonglong2(order_key64(d[0][0] + d[1][0]), order_key64(d[0][1] + d[1][1]));
+        if (bo + 1 < b1)
+          *reinterpret_cast<ulonglong2*>(owner + bo) = k2;  // bo is even
+        else if (bo < b1)
+          owner[bo] = k2.x;
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < kQuarter / 4; ++i) {
+        float v[4];
+        unpack<float>(w[i], v);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) d[e >> 1][e & 1] = fma(qm[0][16 * i + c0 + e], static_cast<double>(v[e]), d[e >> 1][e & 1]);
+      }
+      double s = (d[0][0] + d[0][1]) + (d[1][0] + d[1][1]);
+      s += __shfl_xor_sync(0xffffffffu, s, 1);
+      s += __shfl_xor_sync(0xffffffffu, s, 2);
+      if ((lane & 3) == 0 && t + sub < b1) owner[t + sub] = order_key64(s);
     }
   }
   cluster.sync();
@@ -224,20 +275,21 @@ __global__ void __launch_bounds__(kSelThreads) block_select_kernel(const BlockSe
 
 template <typename T, int HD>
 cudaError_t select_hd(const BlockSelectLaunch& a, cudaStream_t s, int* n) {
-  const int C = (a.groups > 1 || a.n_blocks > 128) ? kSelCluster : 1;
   const size_t smem = sizeof(uint64_t) * static_cast<size_t>(a.n_blocks > 0 ? a.n_blocks : 1);
-  auto kernel = block_select_kernel<T, HD>;
+  const bool al = aligned16(a.q) && a.ld_q * static_cast<int64_t>(sizeof(T)) % 16 == 0;
+  auto kernel = al ? block_select_kernel<T, HD, true> : block_select_kernel<T, HD, false>;
   cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                        static_cast<int>(sizeof(uint64_t) * kMaxBlocks));
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>((a.groups + C - 1) / C * C), static_cast<unsigned>(a.n_heads));
+  cfg.gridDim = dim3(static_cast<unsigned>((a.groups + kSelCluster - 1) / kSelCluster * kSelCluster),
+                     static_cast<unsigned>(a.n_heads));
   cfg.blockDim = dim3(kSelThreads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = s;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = static_cast<unsigned>(C);
+  attr[0].val.clusterDim.x = kSelCluster;
   attr[0].val.clusterDim.y = 1;
   attr[0].val.clusterDim.z = 1;
   cfg.attrs = attr;
@@ -286,7 +338,9 @@ cudaError_t launch_block_means(const BlockMeansLaunch& a, cudaStream_t s, int* n
 
 bool block_select_supported(int64_t n_blocks) { return n_blocks <= kMaxBlocks; }
 
-cudaError_t launch_block_select(const BlockSelectLaunch& a, cudaStream_t s, int* n_launched) {
+cudaError_t launch_block_select(const BlockSelectLaunch& in, cudaStream_t s, int* n_launched) {
+  BlockSelectLaunch a = in;
+  a.means_aligned = aligned16(a.means) && a.ld_means % 4 == 0;
   return a.dtype == 1 ? select_t<float>(a, s, n_launched) : select_t<__nv_bfloat16>(a, s, n_launched);
 }
 

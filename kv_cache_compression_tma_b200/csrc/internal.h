@@ -206,6 +206,7 @@ struct BlockSelectLaunch {
   int64_t ld_means;
   int n_sel;
   int32_t* idx;
+  bool means_aligned;  // set by the launcher: 16-byte aligned rows of means
 };
 bool block_select_supported(int64_t n_blocks);
 cudaError_t launch_block_select(const BlockSelectLaunch& a, cudaStream_t s, int* n_launched);

@@ -510,7 +510,7 @@ ispa_status ispa_block_select(int32_t dtype, int32_t n_heads, int32_t head_dim, 
   if (n_blocks > 0 && (!means || ld_means < d || !aligned(means, 4))) return ISPA_ERR_INVALID_ARG;
   if (!status_ptr()) return ISPA_ERR_CUDA;
   BlockSelectLaunch L{dtype, n_heads, head_dim, q, n_q, ld_q, q_block, (n_q + q_block - 1) / q_block, means,
-                      static_cast<int>(n_blocks), ld_means, n_sel, idx_out};
+                      static_cast<int>(n_blocks), ld_means, n_sel, idx_out, false};
   int n = 0;
   cudaError_t e = launch_block_select(L, static_cast<cudaStream_t>(stream), &n);
   count(n);

@@ -2,10 +2,20 @@
 //
 //   mass_out[h, j] = decay * mass[h, j] + sum_i exp(scale q_i.k_j + b_j - L_i),
 //   L_i = log(exp(lse_loc_i) + exp(lse_hist_i)),
-// for few queries (single-token steps, bf16) and for every fp32 call.  A row of K sits in registers
+// for few queries (single-token steps, bf16) and for every fp32 call.  K is read once whatever n_q is.
+//
+// Up to 8 bf16 queries: a warp takes 16 keys at a time, their rows go from memory straight into the
+// fragments of mma.m16n8k16 (8 query columns cost the same as one), and the next 16 keys are loaded
+// while the present ones are worked on.  Bound by the read of K: the same sums by multiply-adds and
+// shuffles took 53 instructions a key and issue, not memory, set the pace.
+// Otherwise (fp32, unaligned rows, more queries than that on CUDA cores): a key row sits in registers
 // across kLanes lanes (16 bytes each), kRows rows per lane group; the queries pass by in shared-memory
-// tiles as fp32 with their L_i, so K is read once whatever n_q is.  One query: bound by the read of K.
+// tiles as fp32 with their L_i.  Few queries: every warp has keys of its own.  Many: the CTA's eight
+// warps share one warp's keys and take an eighth of the queries each, their sums joined in a fixed
+// order, so that a small cache still spreads over the SMs; bound by the arithmetic.
 #include <math.h>
+
+#include <algorithm>
 
 #include "internal.h"
 #include "mass.cuh"
@@ -16,35 +26,119 @@ namespace ispa {
 namespace {
 
 constexpr int kThreads = 256;
+constexpr int kWarps = kThreads / 32;
 constexpr int kRows = 4;    // keys per lane group and step: 4 independent 16-byte loads per lane
-constexpr int kSteps = 4;   // steps per CTA
-constexpr int kQTile = 16;  // queries staged at a time
+constexpr int kSteps = 4;   // steps per CTA (few queries)
+constexpr int kQTile = 32;  // queries staged at a time
 
-template <typename T, int HD, bool kAligned>
+// ---------------------------------------------------------------- up to 8 bf16 queries
+template <int HD>
+__global__ void __launch_bounds__(kThreads, 2) mass_few_kernel(const MassLaunch a, int ctas_per_head) {
+  using M = Mma16<HD>;
+  const int head = static_cast<int>(blockIdx.x % a.n_heads);  // heads first: CTAs that run together share rows
+  const int cta = static_cast<int>(blockIdx.x / a.n_heads);
+  const int warp = threadIdx.x >> 5, g = (threadIdx.x & 31) >> 2, c = threadIdx.x & 3;
+  const auto* K = static_cast<const __nv_bfloat16*>(a.k) + static_cast<int64_t>(head) * HD + 8 * c;
+  const auto* Q = static_cast<const __nv_bfloat16*>(a.q) + static_cast<int64_t>(head) * HD + 8 * c;
+  const int64_t units = (a.n_k + 15) / 16, stride = static_cast<int64_t>(ctas_per_head) * kWarps;
+  int64_t u = static_cast<int64_t>(cta) * kWarps + warp;
+  if (u >= units) return;
+  auto load = [&](int64_t unit, M& m) {  // rows past the end repeat the last key
+    m.load(K + min(unit * 16 + g, a.n_k - 1) * a.ld_k, K + min(unit * 16 + g + 8, a.n_k - 1) * a.ld_k);
+  };
+  M cur, next;
+  load(u, cur);
+  uint4 q[M::kPieces];
+#pragma unroll
+  for (int j = 0; j < M::kPieces; ++j)
+    q[j] = g < a.n_q ? load_raw<__nv_bfloat16, false>(Q + g * a.ld_q + 32 * j) : make_uint4(0, 0, 0, 0);
+  // this lane's two query columns
+  constexpr float kLog2e = 1.4426950408889634f;
+  const float sl2 = a.scale * kLog2e;
+  bool live[2];
+  float nl[2];
+#pragma unroll
+  for (int x = 0; x < 2; ++x) {
+    const int i = 2 * c + x;
+    live[x] = i < a.n_q;
+    const int64_t o = static_cast<int64_t>(head) * a.n_q + (live[x] ? i : 0);
+    nl[x] = -kLog2e * mass_row_lse(a.lse_loc[o], a.lse_hist ? a.lse_hist[o] : -INFINITY);
+  }
+  for (; u < units; u += stride) {
+    if (u + stride < units) load(u + stride, next);
+    float d[4];
+    cur.scores(q, d);
+    float lo = 0.f, hi = 0.f;
+#pragma unroll
+    for (int x = 0; x < 2; ++x)
+      if (live[x]) {
+        lo += fast_exp2(fmaf(d[x], sl2, nl[x]));
+        hi += fast_exp2(fmaf(d[2 + x], sl2, nl[x]));
+      }
+    lo = row_sum<4>(lo);
+    hi = row_sum<4>(hi);
+    const int64_t j = u * 16 + g + 8 * c;
+    if (c < 2 && j < a.n_k) {
+      float w = c ? hi : lo;
+      const int64_t o = static_cast<int64_t>(head) * a.ld_mass + j;
+      if (a.bias) w = mass_apply_bias(w, a.bias[static_cast<int64_t>(head) * a.ld_bias + j]);
+      a.mass_out[o] = a.decay != 0.f ? fmaf(a.decay, a.mass[o], w) : w;
+    }
+    cur = next;
+  }
+}
+
+template <int HD>
+cudaError_t launch_few(const MassLaunch& a, cudaStream_t s, int* n) {
+  // all CTAs at once (two per SM), none with less than one unit per warp
+  const int64_t units = (a.n_k + 15) / 16;
+  const int64_t per_head = 296 / a.n_heads > 0 ? 296 / a.n_heads : 1;
+  const int ctas = static_cast<int>(std::min(per_head, (units + kWarps - 1) / kWarps));
+  mass_few_kernel<HD><<<static_cast<unsigned>(ctas) * static_cast<unsigned>(a.n_heads), kThreads, 0, s>>>(a, ctas);
+  *n += 1;
+  return cudaGetLastError();
+}
+
+// ---------------------------------------------------------------- any case
+// kSplit: the warps split the queries (one step per CTA); else they split the keys.
+template <typename T, int HD, bool kAligned, bool kSplit>
 __global__ void __launch_bounds__(kThreads) mass_rows_kernel(const MassLaunch a) {
   using R = Row<T, HD>;
-  constexpr int kGroups = kThreads / R::kLanes;
-  constexpr int kKeys = kGroups * kRows;  // keys per step of a CTA
+  constexpr int kWarpKeys = R::kPerWarp * kRows;
+  constexpr int kKeys = kSplit ? kWarpKeys : kWarps * kWarpKeys;  // keys per step of a CTA
   __shared__ float sq[kQTile][HD];
   __shared__ float sl[kQTile];
-  const int head = blockIdx.y;
-  const int group = threadIdx.x / R::kLanes, lane = threadIdx.x % R::kLanes;
+  __shared__ float part[kSplit ? kWarps : 1][kWarpKeys];
+  const int head = static_cast<int>(blockIdx.x % a.n_heads);  // heads first: CTAs that run together share rows
+  const int64_t chunk = blockIdx.x / a.n_heads;
+  const int warp = threadIdx.x >> 5;
+  const int group = (threadIdx.x & 31) / R::kLanes, lane = (threadIdx.x & 31) % R::kLanes;
   const T* K = static_cast<const T*>(a.k) + static_cast<int64_t>(head) * HD + lane * R::kVec;
   const T* Q = static_cast<const T*>(a.q) + static_cast<int64_t>(head) * HD;
-  for (int step = 0; step < kSteps; ++step) {
-    const int64_t j0 = (static_cast<int64_t>(blockIdx.x) * kSteps + step) * kKeys + group * kRows;
-    if (j0 - group * kRows >= a.n_k) break;  // uniform over the CTA
-    uint4 kw[kRows];
+  const int64_t first = chunk * (kSplit ? 1 : kSteps) * kKeys;
+  const int steps = kSplit ? 1 : static_cast<int>(min(static_cast<int64_t>(kSteps), (a.n_k - first + kKeys - 1) / kKeys));
+  auto key_of = [&](int step, int r) {
+    return first + step * kKeys + (kSplit ? 0 : warp * kWarpKeys) + r * R::kPerWarp + group;
+  };
+  auto load = [&](int step, uint4* kw) {
 #pragma unroll
     for (int r = 0; r < kRows; ++r) {
-      const int64_t j = j0 + r < a.n_k ? j0 + r : a.n_k - 1;  // rows past the end repeat the last key
+      const int64_t j = min(key_of(step, r), a.n_k - 1);  // rows past the end repeat the last key
       kw[r] = load_raw<T, kAligned>(K + j * a.ld_k);
     }
+  };
+  uint4 next[kRows];
+  load(0, next);
+  for (int step = 0; step < steps; ++step) {
+    uint4 kw[kRows];
+#pragma unroll
+    for (int r = 0; r < kRows; ++r) kw[r] = next[r];
+    if (step + 1 < steps) load(step + 1, next);
     float sum[kRows] = {};
     for (int64_t i0 = 0; i0 < a.n_q; i0 += kQTile) {
       const int nq = static_cast<int>(a.n_q - i0 < kQTile ? a.n_q - i0 : kQTile);
-      if (i0 > 0 || step == 0 || a.n_q > kQTile) {  // one tile of queries stays staged over the steps
-        __syncthreads();
+      if (step == 0 || a.n_q > kQTile) {  // a lone tile of queries stays staged over the steps
+        if (i0 > 0 || step > 0) __syncthreads();
         for (int x = threadIdx.x; x < nq * HD; x += kThreads)
           sq[x / HD][x % HD] = static_cast<float>(Q[(i0 + x / HD) * a.ld_q + x % HD]) * a.scale;
         if (threadIdx.x < nq) {
@@ -53,13 +147,14 @@ __global__ void __launch_bounds__(kThreads) mass_rows_kernel(const MassLaunch a)
         }
         __syncthreads();
       }
-      for (int i = 0; i < nq; ++i) {
+      for (int i = kSplit ? warp : 0; i < nq; i += kSplit ? kWarps : 1) {
         float qv[R::kVec];
 #pragma unroll
         for (int e = 0; e < R::kVec; e += 4) {
           const float4 w = *reinterpret_cast<const float4*>(&sq[i][lane * R::kVec + e]);
           qv[e] = w.x, qv[e + 1] = w.y, qv[e + 2] = w.z, qv[e + 3] = w.w;
         }
+        const float li = sl[i];
 #pragma unroll
         for (int r = 0; r < kRows; ++r) {
           float kv[R::kVec], s = 0.f;
@@ -67,32 +162,55 @@ __global__ void __launch_bounds__(kThreads) mass_rows_kernel(const MassLaunch a)
 #pragma unroll
           for (int e = 0; e < R::kVec; ++e) s = fmaf(qv[e], kv[e], s);
           s = row_sum<R::kLanes>(s);
-          sum[r] += expf(s - sl[i]);
+          sum[r] += expf(s - li);
         }
       }
     }
+    if constexpr (kSplit) {
 #pragma unroll
-    for (int r = 0; r < kRows; ++r) {
-      const int64_t j = j0 + r;
-      if (lane != r % R::kLanes || j >= a.n_k) continue;
+      for (int r = 0; r < kRows; ++r)
+        if (lane == 0) part[warp][r * R::kPerWarp + group] = sum[r];
+      __syncthreads();
+    }
+    // a lane group's r-th key belongs to its lane r (in the split form to the first warp's threads)
+    auto put = [&](int64_t j, float w) {
+      if (j >= a.n_k) return;
       const int64_t o = static_cast<int64_t>(head) * a.ld_mass + j;
-      float w = sum[r];
       if (a.bias) w = mass_apply_bias(w, a.bias[static_cast<int64_t>(head) * a.ld_bias + j]);
       a.mass_out[o] = a.decay != 0.f ? fmaf(a.decay, a.mass[o], w) : w;
+    };
+    if constexpr (kSplit) {
+      for (int x = threadIdx.x; x < kWarpKeys; x += kThreads) {
+        float w = 0.f;
+#pragma unroll
+        for (int v = 0; v < kWarps; ++v) w += part[v][x];
+        put(first + x, w);
+      }
+    } else {
+#pragma unroll
+      for (int r = 0; r < kRows; ++r)
+        if (lane == r % R::kLanes) put(key_of(step, r), sum[r]);
     }
   }
 }
 
-template <typename T, int HD>
-cudaError_t launch_hd(const MassLaunch& a, cudaStream_t s, int* n) {
-  constexpr int kKeys = kThreads / Row<T, HD>::kLanes * kRows * kSteps;
-  const dim3 grid(static_cast<unsigned>((a.n_k + kKeys - 1) / kKeys), static_cast<unsigned>(a.n_heads));
+template <typename T, int HD, bool kSplit>
+cudaError_t launch_split(const MassLaunch& a, cudaStream_t s, int* n) {
+  constexpr int kKeys = Row<T, HD>::kPerWarp * kRows * (kSplit ? 1 : kWarps * kSteps);
+  const int64_t blocks = (a.n_k + kKeys - 1) / kKeys * a.n_heads;
+  if (blocks > INT32_MAX) return cudaErrorInvalidConfiguration;
+  const unsigned grid = static_cast<unsigned>(blocks);
   if (aligned16(a.k) && (a.ld_k * static_cast<int64_t>(sizeof(T))) % 16 == 0)
-    mass_rows_kernel<T, HD, true><<<grid, kThreads, 0, s>>>(a);
+    mass_rows_kernel<T, HD, true, kSplit><<<grid, kThreads, 0, s>>>(a);
   else
-    mass_rows_kernel<T, HD, false><<<grid, kThreads, 0, s>>>(a);
+    mass_rows_kernel<T, HD, false, kSplit><<<grid, kThreads, 0, s>>>(a);
   *n += 1;
   return cudaGetLastError();
+}
+
+template <typename T, int HD>
+cudaError_t launch_hd(const MassLaunch& a, cudaStream_t s, int* n) {
+  return a.n_q > kWarps ? launch_split<T, HD, true>(a, s, n) : launch_split<T, HD, false>(a, s, n);
 }
 
 template <typename T>
@@ -112,6 +230,8 @@ cudaError_t launch_t(const MassLaunch& a, cudaStream_t s, int* n) {
 }  // namespace
 
 cudaError_t launch_mass_rows(const MassLaunch& a, cudaStream_t s, int* n_launched) {
+  if (a.dtype == 0 && a.n_q >= 1 && a.n_q <= 8 && (a.head_dim == 64 || a.head_dim == 128) && aligned16(a.k) && a.ld_k % 8 == 0)
+    return a.head_dim == 128 ? launch_few<128>(a, s, n_launched) : launch_few<64>(a, s, n_launched);
   return a.dtype == 1 ? launch_t<float>(a, s, n_launched) : launch_t<__nv_bfloat16>(a, s, n_launched);
 }
 

@@ -60,6 +60,42 @@ __device__ __forceinline__ float row_sum(float x) {
   return x;
 }
 
+// D (16 x 8, fp32) += A (16 x 16) B (16 x 8), bf16.  Lane l = 4 g + c holds rows g and g + 8 of A (a0, a2 and
+// a1, a3), column g of B, and D[g][2c, 2c+1] (d0, d1), D[g + 8][2c, 2c+1] (d2, d3).  The order of the 16
+// products is free as long as A and B agree, so a lane may feed any four elements of its row per step.
+__device__ __forceinline__ void mma_bf16(float* d, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                         uint32_t b1) {
+  asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+               : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+               : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// Scores of 16 bf16 key rows against up to 8 query rows, operands straight from memory: piece j of a
+// lane is the 16 bytes (4 j + c) of its row, so four lanes cover 64 contiguous bytes.
+template <int HD>
+struct Mma16 {
+  static constexpr int kPieces = HD / 32;
+  uint4 lo[kPieces], hi[kPieces];  // key rows g and g + 8
+  // row_lo, row_hi: the lane's two rows, offset by 8 c elements
+  __device__ __forceinline__ void load(const __nv_bfloat16* row_lo, const __nv_bfloat16* row_hi) {
+#pragma unroll
+    for (int j = 0; j < kPieces; ++j) lo[j] = __ldg(reinterpret_cast<const uint4*>(row_lo + 32 * j));
+#pragma unroll
+    for (int j = 0; j < kPieces; ++j) hi[j] = __ldg(reinterpret_cast<const uint4*>(row_hi + 32 * j));
+  }
+  __device__ __forceinline__ void scores(const uint4* q, float* d) const {
+    float e[4] = {};  // two chains
+    d[0] = d[1] = d[2] = d[3] = 0.f;
+#pragma unroll
+    for (int j = 0; j < kPieces; ++j) {
+      mma_bf16(d, lo[j].x, hi[j].x, lo[j].y, hi[j].y, q[j].x, q[j].y);
+      mma_bf16(e, lo[j].z, hi[j].z, lo[j].w, hi[j].w, q[j].z, q[j].w);
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) d[i] += e[i];
+  }
+};
+
 inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
 
 }  // namespace ispa

@@ -162,22 +162,63 @@ def _ptr(t) -> Optional[int]:
 
 def _row_stride(t, what: str) -> int:
     """Token/row stride of a [tokens, H, hd] or [rows, d] tensor whose inner dims are dense."""
-    if t.dim() == 3:
-        if t.stride(2) != 1 or t.stride(1) != t.shape[2]:
+    shape, stride = t.shape, t.stride()
+    if len(shape) == 3:
+        if stride[2] != 1 or stride[1] != shape[2]:
             raise ValueError(f"{what}: heads and head_dim must be contiguous")
-    elif t.dim() == 2:
-        if t.stride(1) != 1:
+    elif len(shape) == 2:
+        if stride[1] != 1:
             raise ValueError(f"{what}: columns must be contiguous")
     else:
         raise ValueError(f"{what}: expected 2 or 3 dims")
-    if t.shape[0] <= 1:  # a single row: its stride is irrelevant, report the dense row length
-        return int(np.prod(t.shape[1:]))
-    return int(t.stride(0))
+    if shape[0] <= 1:  # a single row: its stride is irrelevant, report the dense row length
+        return math.prod(shape[1:])
+    return stride[0]
 
 
-def _attn_args(q, k_sink, v_sink, k_loc, v_loc, k_hist, v_hist, o_loc, o_full, lse_loc, lse_hist, d_out, want_delta,
-               softmax_scale, cuda_cores, kv_bias):
-    """The argument block of an attention call, and its outputs (allocated where not given)."""
+def _heads_rows(t, what: str, H: int, hd: int, dtype, device: int, n: Optional[int] = None):
+    """(tokens, token stride) of a [tokens, H, hd] tensor of this type on the current device whose heads
+    and head_dim are dense; n: how many tokens it must have."""
+    shape = t.shape
+    if len(shape) != 3 or shape[1] != H or shape[2] != hd or t.dtype != dtype or (n is not None and shape[0] != n):
+        raise ValueError(f"{what}: expected {dtype} [{'tokens' if n is None else n}, {H}, {hd}]")
+    if t.get_device() != device:
+        _on_current_device(t)
+    stride = t.stride()
+    if stride[2] != 1 or (stride[1] != hd and H > 1):
+        raise ValueError(f"{what}: heads and head_dim must be contiguous")
+    return shape[0], stride[0] if shape[0] > 1 else H * hd
+
+
+def _state_rows(t, what: str, H: int, cols: int, dtype, device: int) -> int:
+    """Row stride of a per-head array [H, >= cols] of this type on the current device, columns contiguous."""
+    shape, stride = t.shape, t.stride()
+    if len(shape) != 2 or shape[0] != H or shape[1] < cols or t.dtype != dtype or (stride[1] != 1 and shape[1] > 1):
+        raise ValueError(f"{what}: expected {dtype} [{H}, >= {cols}] with contiguous columns")
+    if t.get_device() != device:
+        _on_current_device(t)
+    return stride[0] if H > 1 else max(shape[1], 1)
+
+
+def _dense(t, what: str, shape, dtype, device: int) -> int:
+    """Address of a contiguous array of this shape and type on the current device."""
+    if t.shape != shape or t.dtype != dtype or not t.is_contiguous():
+        raise ValueError(f"{what}: expected contiguous {dtype} {list(shape)}")
+    if t.get_device() != device:
+        _on_current_device(t)
+    return t.data_ptr()
+
+
+def dual_stream_attn(q, k_sink, v_sink, k_loc, v_loc, k_hist, v_hist, *, o_loc=None, o_full=None, lse_loc=None,
+                     lse_hist=None, d_out=None, want_delta: bool = True, softmax_scale: float = 0.0,
+                     cuda_cores: bool = False, kv_bias=(None, None, None), stream=None) -> dict:
+    """ispa_dual_stream_attn on torch CUDA tensors.
+
+    q, k_*, v_*: [tokens, H, hd] (bf16 or fp32).  Outputs (allocated if not given): o_loc, o_full and
+    (if want_delta) d = O_full - O_loc as [n_q, H*hd] in q's dtype; lse_loc, lse_hist fp32 [H, n_q].
+    kv_bias: optional per-segment fp32 [H, n_kv] additive logit biases (natural log), e.g. the log group
+    sizes of a TempCache-merged history.
+    """
     import torch
     _on_current_device(q, k_sink, v_sink, k_loc, v_loc, k_hist, v_hist, o_loc, o_full, lse_loc, lse_hist, d_out,
                        *kv_bias)
@@ -194,46 +235,26 @@ def _attn_args(q, k_sink, v_sink, k_loc, v_loc, k_hist, v_hist, o_loc, o_full, l
         lse_loc = torch.empty((H, n_q), dtype=torch.float32, device=dev)
     if lse_hist is None:
         lse_hist = torch.empty((H, n_q), dtype=torch.float32, device=dev)
-    a = AttnArgs()
-    a.dtype = _dtype_code(q)
-    a.n_heads, a.head_dim = H, hd
-    a.flags = ISPA_ATTN_CUDA_CORES if cuda_cores else 0
-    a.n_q = n_q
-    a.q, a.ld_q = _ptr(q), _row_stride(q, "q") if n_q else d
-    for i, (k, v) in enumerate(((k_sink, v_sink), (k_loc, v_loc), (k_hist, v_hist))):
-        a.n_kv[i] = k.shape[0]
-        if k.shape[0]:
-            a.k[i], a.v[i] = _ptr(k), _ptr(v)
-            a.ld_k[i], a.ld_v[i] = _row_stride(k, "k"), _row_stride(v, "v")
-        else:
-            a.k[i] = a.v[i] = None
-            a.ld_k[i] = a.ld_v[i] = d
-    a.softmax_scale = float(softmax_scale)
-    a.o_loc, a.o_full, a.d_out = _ptr(o_loc), _ptr(o_full), _ptr(d_out)
-    a.ld_o = _row_stride(o_loc, "o_loc") if n_q else d
-    a.lse_loc, a.lse_hist = _ptr(lse_loc), _ptr(lse_hist)
+    n_kv, k_ptr, v_ptr, ld_k, ld_v = [], [], [], [], []
+    for k, v in ((k_sink, v_sink), (k_loc, v_loc), (k_hist, v_hist)):
+        n = k.shape[0]
+        n_kv.append(n)
+        k_ptr.append(k.data_ptr() if n else None)
+        v_ptr.append(v.data_ptr() if n else None)
+        ld_k.append(_row_stride(k, "k") if n else d)
+        ld_v.append(_row_stride(v, "v") if n else d)
+    bias, ld_bias = [None] * 3, [0] * 3
     for i, bt in enumerate(kv_bias):
         if bt is not None:
             if bt.dtype != torch.float32 or bt.dim() != 2 or bt.stride(1) != 1:
                 raise ValueError("kv_bias entries must be fp32 [H, n_kv] with contiguous columns")
-            a.kv_bias[i], a.ld_bias[i] = _ptr(bt), int(bt.stride(0))
-    return a, {"o_loc": o_loc, "o_full": o_full, "d": d_out, "lse_loc": lse_loc, "lse_hist": lse_hist}
-
-
-def dual_stream_attn(q, k_sink, v_sink, k_loc, v_loc, k_hist, v_hist, *, o_loc=None, o_full=None, lse_loc=None,
-                     lse_hist=None, d_out=None, want_delta: bool = True, softmax_scale: float = 0.0,
-                     cuda_cores: bool = False, kv_bias=(None, None, None), stream=None) -> dict:
-    """ispa_dual_stream_attn on torch CUDA tensors.
-
-    q, k_*, v_*: [tokens, H, hd] (bf16 or fp32).  Outputs (allocated if not given): o_loc, o_full and
-    (if want_delta) d = O_full - O_loc as [n_q, H*hd] in q's dtype; lse_loc, lse_hist fp32 [H, n_q].
-    kv_bias: optional per-segment fp32 [H, n_kv] additive logit biases (natural log), e.g. the log group
-    sizes of a TempCache-merged history.
-    """
-    a, out = _attn_args(q, k_sink, v_sink, k_loc, v_loc, k_hist, v_hist, o_loc, o_full, lse_loc, lse_hist, d_out,
-                        want_delta, softmax_scale, cuda_cores, kv_bias)
+            bias[i], ld_bias[i] = bt.data_ptr(), bt.stride(0)
+    a = AttnArgs(_dtype_code(q), H, hd, ISPA_ATTN_CUDA_CORES if cuda_cores else 0, n_q, tuple(n_kv), q.data_ptr(),
+                 _row_stride(q, "q") if n_q else d, tuple(k_ptr), tuple(v_ptr), tuple(ld_k), tuple(ld_v),
+                 softmax_scale, 0.0, o_loc.data_ptr(), o_full.data_ptr(), _row_stride(o_loc, "o_loc") if n_q else d,
+                 lse_loc.data_ptr(), lse_hist.data_ptr(), _ptr(d_out), tuple(bias), tuple(ld_bias))
     _check(lib().ispa_dual_stream_attn(ctypes.byref(a), _stream(stream)), "ispa_dual_stream_attn")
-    return out
+    return {"o_loc": o_loc, "o_full": o_full, "d": d_out, "lse_loc": lse_loc, "lse_hist": lse_hist}
 
 
 def accum_stats(a_loc, a_second, G, R, S, *, second_is_full: bool = False, zero: bool = False, stream=None):
@@ -414,18 +435,6 @@ class TempCache:
         return self.k[:n], self.v[:n], self.bias[:, :n]
 
 
-def _state_stride(t, what: str, heads: int, cols: int, dtype) -> int:
-    """Row stride of a per-head state array [H, >= cols] with contiguous columns."""
-    if t.dim() != 2 or t.dtype != dtype or t.shape[0] != heads or t.shape[1] < cols or (t.shape[1] > 1 and t.stride(1) != 1):
-        raise ValueError(f"{what}: expected {dtype} [{heads}, >= {cols}] with contiguous columns")
-    return int(t.stride(0)) if heads > 1 else max(int(t.shape[1]), 1)
-
-
-def _heads_like(t, what: str, heads: int, head_dim: int, dtype):
-    if t.dim() != 3 or t.shape[1] != heads or t.shape[2] != head_dim or t.dtype != dtype:
-        raise ValueError(f"{what}: expected {dtype} [tokens, {heads}, {head_dim}]")
-
-
 def attn_mass(q, k, lse_loc, lse_hist, mass, *, kv_bias=None, decay: float = 1.0, softmax_scale: float = 0.0,
               cuda_cores: bool = False, mass_out=None, stream=None):
     """ispa_attn_mass: mass[h, j] = decay * mass[h, j] + the attention weight that key j collects from the
@@ -434,23 +443,22 @@ def attn_mass(q, k, lse_loc, lse_hist, mass, *, kv_bias=None, decay: float = 1.0
     kv_bias: fp32 [H, >= n_k], the segment's bias in that call.  mass fp32 [H, >= n_k]; the result goes to
     mass_out (same shape and stride as mass) or back into mass.  Returns the array written."""
     import torch
-    _on_current_device(q, k, lse_loc, lse_hist, mass, kv_bias, mass_out)
+    f32, dev = torch.float32, torch.cuda.current_device()
     n_q, H, hd = q.shape
-    n_k = k.shape[0]
-    _heads_like(k, "k", H, hd, q.dtype)
-    for t in (lse_loc, lse_hist):
-        if t is not None and (t.dtype != torch.float32 or tuple(t.shape) != (H, n_q) or not t.is_contiguous()):
-            raise ValueError("lse_loc and lse_hist must be contiguous fp32 [H, n_q]")
-    ld_mass = _state_stride(mass, "mass", H, n_k, torch.float32)
+    dtype = q.dtype
+    _, ld_q = _heads_rows(q, "q", H, hd, dtype, dev)
+    n_k, ld_k = _heads_rows(k, "k", H, hd, dtype, dev)
+    ll = _dense(lse_loc, "lse_loc", (H, n_q), f32, dev)
+    lh = None if lse_hist is None else _dense(lse_hist, "lse_hist", (H, n_q), f32, dev)
+    ld_mass = _state_rows(mass, "mass", H, n_k, f32, dev)
     if mass_out is None:
         mass_out = mass
-    elif _state_stride(mass_out, "mass_out", H, n_k, torch.float32) != ld_mass:
+    elif _state_rows(mass_out, "mass_out", H, n_k, f32, dev) != ld_mass:
         raise ValueError("mass and mass_out must share a row stride")
-    ld_bias = 0 if kv_bias is None else _state_stride(kv_bias, "kv_bias", H, n_k, torch.float32)
-    _check(lib().ispa_attn_mass(_dtype_code(q), H, hd, _ptr(q), n_q, _row_stride(q, "q"), _ptr(k), n_k,
-                                _row_stride(k, "k"), _ptr(lse_loc), _ptr(lse_hist), _ptr(kv_bias), ld_bias,
-                                softmax_scale, decay, ISPA_ATTN_CUDA_CORES if cuda_cores else 0, _ptr(mass),
-                                _ptr(mass_out), ld_mass, _stream(stream)), "ispa_attn_mass")
+    bias, ld_bias = (None, 0) if kv_bias is None else (kv_bias.data_ptr(), _state_rows(kv_bias, "kv_bias", H, n_k, f32, dev))
+    _check(lib().ispa_attn_mass(_dtype_code(q), H, hd, q.data_ptr(), n_q, ld_q, k.data_ptr(), n_k, ld_k, ll, lh, bias,
+                                ld_bias, softmax_scale, decay, ISPA_ATTN_CUDA_CORES if cuda_cores else 0,
+                                mass.data_ptr(), mass_out.data_ptr(), ld_mass, _stream(stream)), "ispa_attn_mass")
     return mass_out
 
 
@@ -465,28 +473,35 @@ def cache_insert(k_cache, v_cache, mass, pos, n: int, k_new, v_new, mass_new, po
     of least weight leave.  Positions below keep_below or from keep_from on are protected.  The state
     goes to mass_out, pos_out or back into mass, pos.  Returns the number of entries held afterwards."""
     import torch
-    _on_current_device(k_cache, v_cache, mass, pos, k_new, v_new, mass_new, mass_out, pos_out)
+    f32, i32, dev = torch.float32, torch.int32, torch.cuda.current_device()
     capacity, H, hd = k_cache.shape
-    n_new = k_new.shape[0]
-    total = min(capacity, n + n_new)
-    for t, what in ((v_cache, "v_cache"), (k_new, "k_new"), (v_new, "v_new")):
-        _heads_like(t, what, H, hd, k_cache.dtype)
-    if v_cache.shape[0] != capacity or v_new.shape[0] != n_new:
-        raise ValueError("k and v must have the same number of tokens")
-    ld_cache, ld_new = _row_stride(k_cache, "k_cache"), _row_stride(k_new, "k_new")
-    if _row_stride(v_cache, "v_cache") != ld_cache or _row_stride(v_new, "v_new") != ld_new:
+    dtype = k_cache.dtype
+    _, ld_cache = _heads_rows(k_cache, "k_cache", H, hd, dtype, dev)
+    n_new, ld_new = _heads_rows(k_new, "k_new", H, hd, dtype, dev)
+    if _heads_rows(v_cache, "v_cache", H, hd, dtype, dev, capacity)[1] != ld_cache or \
+            _heads_rows(v_new, "v_new", H, hd, dtype, dev, n_new)[1] != ld_new:
         raise ValueError("k and v must share a row stride")
-    mass_out = mass if mass_out is None else mass_out
-    pos_out = pos if pos_out is None else pos_out
-    ld_state = _state_stride(mass, "mass", H, n, torch.float32)
-    ld_out = _state_stride(mass_out, "mass_out", H, total, torch.float32)
-    if _state_stride(pos, "pos", H, n, torch.int32) != ld_state or _state_stride(pos_out, "pos_out", H, total, torch.int32) != ld_out:
+    total = min(capacity, n + n_new)
+    ld_state = _state_rows(mass, "mass", H, n, f32, dev)
+    ld_out = ld_state
+    same = _state_rows(pos, "pos", H, n, i32, dev) == ld_state
+    if mass_out is None:
+        mass_out = mass
+    else:
+        ld_out = _state_rows(mass_out, "mass_out", H, total, f32, dev)
+    if pos_out is None:
+        pos_out = pos
+    else:
+        same = same and _state_rows(pos_out, "pos_out", H, total, i32, dev) == ld_out
+    if not same:
         raise ValueError("mass and pos (mass_out and pos_out) must share a row stride")
-    ld_mass_new = 0 if mass_new is None else _state_stride(mass_new, "mass_new", H, n_new, torch.float32)
-    _check(lib().ispa_cache_insert(_dtype_code(k_cache), H, hd, _ptr(k_cache), _ptr(v_cache), ld_cache, capacity, n,
-                                   _ptr(mass), _ptr(pos), ld_state, _ptr(k_new), _ptr(v_new), n_new, ld_new,
-                                   _ptr(mass_new), ld_mass_new, pos_new, keep_below, keep_from, _ptr(mass_out),
-                                   _ptr(pos_out), ld_out, _stream(stream)), "ispa_cache_insert")
+    if mass.shape[1] < total and mass_out is mass or pos.shape[1] < total and pos_out is pos:
+        raise ValueError(f"mass and pos need room for {total} entries per head")
+    mn, ld_mn = (None, 0) if mass_new is None else (mass_new.data_ptr(), _state_rows(mass_new, "mass_new", H, n_new, f32, dev))
+    _check(lib().ispa_cache_insert(_dtype_code(k_cache), H, hd, k_cache.data_ptr(), v_cache.data_ptr(), ld_cache, capacity,
+                                   n, mass.data_ptr(), pos.data_ptr(), ld_state, k_new.data_ptr(), v_new.data_ptr(),
+                                   n_new, ld_new, mn, ld_mn, pos_new, keep_below, keep_from, mass_out.data_ptr(),
+                                   pos_out.data_ptr(), ld_out, _stream(stream)), "ispa_cache_insert")
     return total
 
 
@@ -528,13 +543,14 @@ def block_means(k, means, block: int, *, first: int = 0, stream=None):
     """ispa_block_means: means[b] (fp32 [>= blocks, H, hd]) = mean key of block b of k [n_k, H, hd], for the
     blocks from `first` on; earlier rows are left as they are."""
     import torch
-    _on_current_device(k, means)
-    n_k, H, hd = k.shape
-    _heads_like(means, "means", H, hd, torch.float32)
-    if means.shape[0] < -(-n_k // block):
+    dev = torch.cuda.current_device()
+    _, H, hd = k.shape
+    n_k, ld_k = _heads_rows(k, "k", H, hd, k.dtype, dev)
+    rows, ld_means = _heads_rows(means, "means", H, hd, torch.float32, dev)
+    if rows < -(-n_k // block):
         raise ValueError("means has fewer rows than k has blocks")
-    _check(lib().ispa_block_means(_dtype_code(k), H, hd, _ptr(k), n_k, _row_stride(k, "k"), block, first, _ptr(means),
-                                  _row_stride(means, "means"), _stream(stream)), "ispa_block_means")
+    _check(lib().ispa_block_means(_dtype_code(k), H, hd, k.data_ptr(), n_k, ld_k, block, first, means.data_ptr(),
+                                  ld_means, _stream(stream)), "ispa_block_means")
     return means
 
 
@@ -542,16 +558,15 @@ def block_select(q, means, n_sel: int, *, q_block: int = 1, out=None, stream=Non
     """ispa_block_select: int32 [H, ceil(n_q / q_block), n_sel], the blocks (rows of means, fp32 [blocks, H,
     hd]) of highest (mean query of the group) . (mean key), ascending, -1 where there are fewer."""
     import torch
-    _on_current_device(q, means, out)
+    dev = torch.cuda.current_device()
     n_q, H, hd = q.shape
-    _heads_like(means, "means", H, hd, torch.float32)
+    _, ld_q = _heads_rows(q, "q", H, hd, q.dtype, dev)
+    n_blocks, ld_means = _heads_rows(means, "means", H, hd, torch.float32, dev)
     shape = (H, -(-n_q // q_block), n_sel)
     if out is None:
         out = torch.empty(shape, dtype=torch.int32, device=q.device)
-    elif out.dtype != torch.int32 or tuple(out.shape) != shape or not out.is_contiguous():
-        raise ValueError(f"out must be contiguous int32 {list(shape)}")
-    _check(lib().ispa_block_select(_dtype_code(q), H, hd, _ptr(q), n_q, _row_stride(q, "q"), q_block, _ptr(means),
-                                   means.shape[0], _row_stride(means, "means"), n_sel, _ptr(out), _stream(stream)),
+    _check(lib().ispa_block_select(_dtype_code(q), H, hd, q.data_ptr(), n_q, ld_q, q_block, means.data_ptr(), n_blocks,
+                                   ld_means, n_sel, _dense(out, "out", shape, torch.int32, dev), _stream(stream)),
            "ispa_block_select")
     return out
 
@@ -581,15 +596,44 @@ def block_sparse_attn(q, k_sink, v_sink, k_loc, v_loc, k_hist, v_hist, idx, *, b
     tokens of k_hist, v_hist) listed in idx, int32 [H, ceil(n_q / q_block), n_sel], for each group of
     q_block queries (as block_select gives them).  The same outputs as dual_stream_attn."""
     import torch
-    a, out = _attn_args(q, k_sink, v_sink, k_loc, v_loc, k_hist, v_hist, o_loc, o_full, lse_loc, lse_hist, d_out,
-                        want_delta, softmax_scale, cuda_cores, (None, None, None))
-    _on_current_device(idx)
-    groups = -(-a.n_q // q_block)
-    if idx.dtype != torch.int32 or idx.dim() != 3 or tuple(idx.shape[:2]) != (a.n_heads, groups) or not idx.is_contiguous():
-        raise ValueError(f"idx must be contiguous int32 [{a.n_heads}, {groups}, n_sel]")
-    _check(lib().ispa_block_sparse_attn(ctypes.byref(a), _ptr(idx), idx.shape[2], block, q_block, _stream(stream)),
-           "ispa_block_sparse_attn")
-    return out
+    dtype, dev, f32 = q.dtype, torch.cuda.current_device(), torch.float32
+    n_q, H, hd = q.shape
+    n_q, ld_q = _heads_rows(q, "q", H, hd, dtype, dev)
+    ns, ld_ks = _heads_rows(k_sink, "k_sink", H, hd, dtype, dev)
+    ld_vs = _heads_rows(v_sink, "v_sink", H, hd, dtype, dev, ns)[1]
+    nl, ld_kl = _heads_rows(k_loc, "k_loc", H, hd, dtype, dev)
+    ld_vl = _heads_rows(v_loc, "v_loc", H, hd, dtype, dev, nl)[1]
+    nh, ld_kh = _heads_rows(k_hist, "k_hist", H, hd, dtype, dev)
+    ld_vh = _heads_rows(v_hist, "v_hist", H, hd, dtype, dev, nh)[1]
+    shape, ld_o = (n_q, H * hd), H * hd
+    if o_loc is None:
+        o_loc = torch.empty(shape, dtype=dtype, device=q.device)
+    elif n_q > 1:
+        ld_o = o_loc.stride()[0]
+    if o_full is None:
+        o_full = torch.empty_strided(shape, (ld_o, 1), dtype=dtype, device=q.device)
+    if d_out is None and want_delta:
+        d_out = torch.empty_strided(shape, (ld_o, 1), dtype=dtype, device=q.device)
+    for o in (o_loc, o_full, d_out):
+        if o is None:
+            continue
+        if o.shape != shape or o.dtype != dtype or (n_q > 1 and o.stride() != (ld_o, 1)):
+            raise ValueError(f"outputs must be {dtype} {list(shape)} with one row stride")
+        if o.get_device() != dev:
+            _on_current_device(o)
+    if lse_loc is None:
+        lse_loc = torch.empty((H, n_q), dtype=f32, device=q.device)
+    if lse_hist is None:
+        lse_hist = torch.empty((H, n_q), dtype=f32, device=q.device)
+    n_sel = idx.shape[-1]
+    a = AttnArgs(_dtype_code(q), H, hd, ISPA_ATTN_CUDA_CORES if cuda_cores else 0, n_q, (ns, nl, nh), q.data_ptr(), ld_q,
+                 (k_sink.data_ptr(), k_loc.data_ptr(), k_hist.data_ptr()),
+                 (v_sink.data_ptr(), v_loc.data_ptr(), v_hist.data_ptr()), (ld_ks, ld_kl, ld_kh), (ld_vs, ld_vl, ld_vh),
+                 softmax_scale, 0.0, o_loc.data_ptr(), o_full.data_ptr(), ld_o,
+                 _dense(lse_loc, "lse_loc", (H, n_q), f32, dev), _dense(lse_hist, "lse_hist", (H, n_q), f32, dev), _ptr(d_out))
+    _check(lib().ispa_block_sparse_attn(ctypes.byref(a), _dense(idx, "idx", (H, -(-n_q // q_block), n_sel), torch.int32, dev),
+                                        n_sel, block, q_block, _stream(stream)), "ispa_block_sparse_attn")
+    return {"o_loc": o_loc, "o_full": o_full, "d": d_out, "lse_loc": lse_loc, "lse_hist": lse_hist}
 
 
 def select_layers(eps: Sequence[float], k: int):
