@@ -525,6 +525,9 @@ ispa_status ispa_block_sparse_attn(const ispa_attn_args* a, const int32_t* idx, 
   if (checked != ISPA_OK) return checked;
   if (n_sel < 0 || block < 1 || block > 65536 || q_block < 1 || a->n_heads > 65535) return ISPA_ERR_INVALID_ARG;
   if (n_sel > 0 && (!idx || !aligned(idx, 4))) return ISPA_ERR_INVALID_ARG;
+  if (static_cast<int64_t>(n_sel) * block > (1ll << 30) || a->n_kv[0] > (1ll << 30) || a->n_kv[1] > (1ll << 30) ||
+      a->n_kv[2] > (1ll << 30))
+    return ISPA_ERR_INVALID_ARG;
   if (biased) return ISPA_ERR_UNSUPPORTED;
   const bool cuda_cores = (a->flags & ISPA_ATTN_CUDA_CORES) != 0 || a->dtype == ISPA_F32;
   const BlockList B{idx, n_sel, block, q_block, (a->n_q + q_block - 1) / q_block,
