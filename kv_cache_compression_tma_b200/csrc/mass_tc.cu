@@ -6,15 +6,26 @@
 // threads and no atomics.
 //
 // Persistent CTAs, one per SM, each with a contiguous range of 128-key tiles.  A CTA takes two tiles of
-// a head at a time (each 128-query tile then serves two products) or, where one is left, a single
-// tile.  The key tiles come by TMA into a staging buffer while the previous ones are worked on, and
-// go into TMEM as the A operand, so the products read only the queries from shared memory; the queries
-// stream through a ring of 128-row tiles; sub-products S_n of 128 keys x 128 queries rotate through
-// three TMEM accumulators, drained by two warpgroups in turn (n % 2, so with two key tiles each
-// warpgroup has the same one throughout).
+// a head at a time (each query tile then serves two products) or, where one is left, a single tile.
+// The key tiles come by TMA into a staging buffer while the previous ones are worked on, and go into
+// TMEM as the first operand, so the products read only the queries from shared memory.  Products of
+// 128 keys x 128 queries rotate through three TMEM accumulators (the rest of TMEM holds the keys),
+// drained by two pairs of warpgroups in turn (with two key tiles a pair always has the same one), 64
+// columns per warpgroup: a thread takes its columns into registers and frees the accumulator before
+// it computes.  Sixteen warps, because the work per element is a chain (scale, exponential, add) whose
+// latency eight do not cover.
 //
-// Warp roles (352 threads): warp 0 TMA producer, warp 1 TMEM and the MMAs, warp 2 idle, warps 3..10 the
-// two warpgroups.  TMEM columns: [0,384) three accumulators, [384,512) two key tiles (bf16 pairs).
+// Bound: the exponentials and the products together, under the power cap.  12 heads x 4680 queries x
+// 14040 keys: 0.204 ms (202 GFLOP, 0.124 ms at the measured bf16 peak; 0.171 ms if the special-function
+// unit did every exponential at 1965 MHz), with 71 % of that unit, 48 % of the multiply-add pipes and
+// 47 % of the tensor pipe busy at a clock of 1.6 to 1.8 GHz.  Measured beside it, 12 heads: 0.246 ms with
+// 8 warps and 0.234 with 16 while a lone lane issued the MMAs (their operands then move to uniform
+// registers one by one; umma_ts_warp), 0.226 without the polynomial exponential, 0.205 with products
+// 192 or 256 queries wide on two accumulators, 0.235 with 96 on four (each completion costs the tensor
+// pipe some 400 clocks).
+//
+// Warp roles (608 threads): warp 0 TMA producer, warp 1 TMEM and the MMAs, warp 2 idle, warps 3..18 the
+// four warpgroups.  TMEM columns: [0,384) three accumulators, [384,512) two key tiles (bf16 pairs).
 // Every barrier wait is bounded (sm100.cuh); one that runs out records ISPA_ERR_TIMEOUT and unwinds.
 #include <math.h>
 #include <string.h>
@@ -27,12 +38,19 @@
 namespace ispa {
 namespace {
 
-constexpr int kTile = 128;       // keys per tile, queries per tile
-constexpr int kStages = 4;       // query tiles in flight
+constexpr int kTile = 128;       // keys per tile
+constexpr int kSub = 128;        // queries per product
 constexpr int kAcc = 3;          // accumulators
-constexpr int kChunk = 8192;     // queries whose -L sits in shared memory at a time
+constexpr int kCols = kSub / 2;  // accumulator columns of a thread
+constexpr int kQTile = 2 * kSub;  // queries per load
+constexpr int kStages = 2;       // query tiles in flight
+constexpr int kChunk = 6144;     // queries whose -L sits in shared memory at a time
 constexpr int kFirstEpiWarp = 3;
-constexpr int kThreads = 32 * kFirstEpiWarp + 256;
+constexpr int kEpiThreads = 512;
+constexpr int kThreads = 32 * kFirstEpiWarp + kEpiThreads;
+// Of eight pairs of queries, those whose exponentials run on the multiply-add pipes, the others on the
+// special-function unit: it alone takes 16 a clock, less than the products deliver.
+constexpr int kPolyPairs = 0b10001000;
 constexpr float kLog2e = 1.4426950408889634f;
 
 struct Params {
@@ -51,19 +69,42 @@ struct Params {
 template <int HD>
 struct Cfg {
   static constexpr int kBoxes = HD / 64;
-  static constexpr int kBoxBytes = kTile * 128;
-  static constexpr int kTileBytes = kTile * HD * 2;
+  static constexpr int kBoxK = kTile * 128, kBoxQ = kQTile * 128;  // 64 columns of a tile
+  static constexpr int kBytesK = kTile * HD * 2, kBytesQ = kQTile * HD * 2;
   static constexpr int kOffQ = 0;
-  static constexpr int kOffK = kStages * kTileBytes;
-  static constexpr int kOffL = kOffK + 2 * kTileBytes;      // [kChunk] -L * log2(e)
+  static constexpr int kOffK = kStages * kBytesQ;
+  static constexpr int kOffL = kOffK + 2 * kBytesK;         // [kChunk] -L * log2(e)
   static constexpr int kOffBar = kOffL + kChunk * 4;
-  // q_full[kStages], q_empty[kStages], acc_full[kAcc], acc_empty[kAcc], k_full, k_staged_free, k_ready, final
+  // q_full[kStages], q_empty[kStages], acc_full[kAcc], acc_empty[kAcc], k_full, k_free, k_ready, final
   static constexpr int kNumBars = 2 * kStages + 2 * kAcc + 4;
-  static constexpr int kOffMisc = kOffBar + kNumBars * 8;
-  static constexpr int kSmemBytes = kOffMisc + 16 + 128 * 4;  // and the second warpgroup's sums of a single tile
-  static constexpr uint32_t kIdesc = idesc_bf16_f32(kTile, kTile, false, false);
+  static constexpr int kOffMisc = kOffBar + kNumBars * 8 + 8;
+  static constexpr int kSmemBytes = kOffMisc + 16 + 2 * 3 * kTile * 4;  // and the warpgroups' sums of an item, by its parity
   static_assert(kSmemBytes <= 232448, "shared memory budget");
 };
+
+// 2^y of a pair, by the fused multiply-add pipes: n = round(y), a polynomial of degree 4 for 2^(y - n) on
+// [-1/2, 1/2] (weighted least squares iterated to equal ripple: largest relative error 2.7e-6, mean
+// 4e-8, so a sum of many loses nothing), and 2^n from n's bits.  Returns the polynomial's value and
+// 2^n apart: the caller's accumulation multiplies them.  y below -127 gives n = -127, whose 2^n is 0;
+// NaN stays NaN.
+__device__ __forceinline__ void exp2_poly2(uint64_t y, uint64_t& p, uint64_t& scale) {
+  float y0, y1;
+  unpack_f2(y, y0, y1);
+  asm("max.NaN.f32 %0, %0, %1;" : "+f"(y0) : "f"(-127.f));
+  asm("max.NaN.f32 %0, %0, %1;" : "+f"(y1) : "f"(-127.f));
+  const uint64_t yc = pack_f2(y0, y1);
+  const uint64_t magic = pack_f2(12582912.f, 12582912.f);  // 1.5 * 2^23: the sum's low mantissa bits are n
+  const uint64_t t = add_f2(yc, magic);
+  const uint64_t n = add_f2(t, pack_f2(-12582912.f, -12582912.f));
+  const uint64_t f = fma_f2(n, pack_f2(-1.f, -1.f), yc);
+  p = fma_f2(pack_f2(9.570102207362652e-3f, 9.570102207362652e-3f), f, pack_f2(5.591785907745361e-2f, 5.591785907745361e-2f));
+  p = fma_f2(p, f, pack_f2(2.40247443318367e-1f, 2.40247443318367e-1f));
+  p = fma_f2(p, f, pack_f2(6.931217908859253e-1f, 6.931217908859253e-1f));
+  p = fma_f2(p, f, pack_f2(9.999992847442627e-1f, 9.999992847442627e-1f));
+  float t0, t1;
+  unpack_f2(t, t0, t1);
+  scale = pack_f2(__uint_as_float((__float_as_uint(t0) << 23) + 0x3f800000u), __uint_as_float((__float_as_uint(t1) << 23) + 0x3f800000u));
+}
 
 // The CTA's tiles [first, last) one or two at a time: two only within a head.
 __device__ __forceinline__ int tiles_at(const Params& p, int t, int last) {
@@ -83,9 +124,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint64_t* q_empty = q_full + kStages;
   uint64_t* acc_full = q_empty + kStages;
   uint64_t* acc_empty = acc_full + kAcc;
-  uint64_t* k_full = acc_empty + kAcc;   // the staging buffer holds the item's key tiles
-  uint64_t* k_free = k_full + 1;         // ... and they are in TMEM
-  uint64_t* k_ready = k_free + 1;        // the same, for the MMA thread
+  uint64_t* k_full = acc_empty + kAcc;  // the staging buffer holds the item's key tiles
+  uint64_t* k_free = k_full + 1;     // ... and they are in TMEM: the buffer may be filled again,
+  uint64_t* k_ready = k_free + 1;    // and the products may start
   uint64_t* final_bar = k_ready + 1;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::kOffMisc);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::kOffMisc + 4);
@@ -93,10 +134,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   float* other = reinterpret_cast<float*>(smem + C::kOffMisc + 16);
   float* neg_l = reinterpret_cast<float*>(smem + C::kOffL);
 
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;  // warp-uniform
   const int first = static_cast<int>(static_cast<int64_t>(p.n_tiles) * blockIdx.x / gridDim.x);
   const int last = static_cast<int>(static_cast<int64_t>(p.n_tiles) * (blockIdx.x + 1) / gridDim.x);
-  const int n_sub = (p.n_q + kTile - 1) / kTile;  // query tiles
+  const int n_sub = (p.n_q + kSub - 1) / kSub;  // products per key tile
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < kStages; ++i) {
@@ -105,11 +146,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     for (int i = 0; i < kAcc; ++i) {
       mbar_init(acc_full + i, 1);
-      mbar_init(acc_empty + i, 4);
+      mbar_init(acc_empty + i, 8);
     }
     mbar_init(k_full, 1);
-    mbar_init(k_free, 8);
-    mbar_init(k_ready, 8);
+    mbar_init(k_free, 16);
+    mbar_init(k_ready, 16);
     mbar_init(final_bar, 1);
     *abort_flag = 0;
     *never = 0;
@@ -129,35 +170,28 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (lane == 0) {
       bool ok = true;
       int item = 0, n_issued = 0, k_issued = 0;
-      auto load_keys = [&](int t, int count) {
-        if (item > 0 && !mbar_wait(k_free, (item - 1) & 1, abort_flag)) return false;
-        mbar_arrive_expect_tx(k_full, count * C::kTileBytes);
-        const int head = t / p.tiles_per_head, key0 = (t % p.tiles_per_head) * kTile;
-        for (int i = 0; i < count; ++i)
-#pragma unroll
-          for (int b = 0; b < C::kBoxes; ++b)
-            tma_load_2d(smem + C::kOffK + i * C::kTileBytes + b * C::kBoxBytes, &map_k, k_full, head * HD + 64 * b,
-                        key0 + i * kTile);
-        ++k_issued;
-        return true;
-      };
       for (int t = first; ok && t < last; ++item) {
-        const int count = tiles_at(p, t, last), head = t / p.tiles_per_head;
-        if (!load_keys(t, count)) {
+        const int count = tiles_at(p, t, last), head = t / p.tiles_per_head, key0 = (t % p.tiles_per_head) * kTile;
+        if (item > 0 && !mbar_wait(k_free, (item - 1) & 1, abort_flag)) {
           ok = false;
           break;
         }
-        for (int n = 0; n < n_sub; ++n) {
+        mbar_arrive_expect_tx(k_full, count * C::kBytesK);
+        for (int i = 0; i < count; ++i)
+#pragma unroll
+          for (int b = 0; b < C::kBoxes; ++b)
+            tma_load_2d(smem + C::kOffK + i * C::kBytesK + b * C::kBoxK, &map_k, k_full, head * HD + 64 * b, key0 + i * kTile);
+        ++k_issued;
+        for (int n = 0; n < n_sub; n += kQTile / kSub) {
           const int s = n_issued % kStages;
           if (n_issued >= kStages && !mbar_wait(q_empty + s, (n_issued / kStages - 1) & 1, abort_flag)) {
             ok = false;
             break;
           }
-          mbar_arrive_expect_tx(q_full + s, C::kTileBytes);
+          mbar_arrive_expect_tx(q_full + s, C::kBytesQ);
 #pragma unroll
           for (int b = 0; b < C::kBoxes; ++b)
-            tma_load_2d(smem + C::kOffQ + s * C::kTileBytes + b * C::kBoxBytes, &map_q, q_full + s, head * HD + 64 * b,
-                        n * kTile);
+            tma_load_2d(smem + C::kOffQ + s * C::kBytesQ + b * C::kBoxQ, &map_q, q_full + s, head * HD + 64 * b, n * kSub);
           ++n_issued;
         }
         t += count;
@@ -175,46 +209,52 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   } else if (warp == 1) {
     // ------------------------------------------------------------------ MMA issuer
-    if (lane == 0) {
+    {
+      const uint32_t leader = elect_leader();
       bool ok = true;
       int item = 0, n_done = 0, seq = 0;
       for (int t = first; ok && t < last; ++item) {
         const int count = tiles_at(p, t, last);
-        ok = mbar_wait(k_ready, item & 1, abort_flag);
-        tc_fence_after();
-        for (int n = 0; ok && n < n_sub; ++n, ++n_done) {
-          const int s = n_done % kStages;
-          ok = mbar_wait(q_full + s, (n_done / kStages) & 1, abort_flag);
-          const uint32_t qb = smem_u32(smem + C::kOffQ + s * C::kTileBytes);
+        ok = mbar_wait_warp(k_ready, item & 1, abort_flag);
+        for (int n = 0; ok && n < n_sub; ++n) {
+          const int s = n_done % kStages, part = n % (kQTile / kSub);
+          if (part == 0) ok = mbar_wait_warp(q_full + s, (n_done / kStages) & 1, abort_flag);
+          const uint32_t qb = smem_u32(smem + C::kOffQ + s * C::kBytesQ + part * kSub * 128);
+          const int width = min(kSub, (p.n_q - n * kSub + 15) / 16 * 16);  // the last one may be narrower
+          const uint32_t idesc = idesc_bf16_f32(kTile, width, false, false);
           for (int i = 0; ok && i < count; ++i, ++seq) {
             const int a = seq % kAcc;
-            if (seq >= kAcc && !mbar_wait(acc_empty + a, (seq / kAcc - 1) & 1, abort_flag)) {
+            if (seq >= kAcc && !mbar_wait_warp(acc_empty + a, (seq / kAcc - 1) & 1, abort_flag)) {
               ok = false;
               break;
             }
             tc_fence_after();
 #pragma unroll
             for (int kk = 0; kk < HD / 16; ++kk)
-              umma_ts(tmem + a * kTile, tmem + kAcc * kTile + i * 64 + kk * 8,
-                      sw128_desc(qb + (kk >> 2) * C::kBoxBytes + (kk & 3) * 32, 16, 1024), C::kIdesc, kk > 0 ? 1u : 0u);
-            umma_commit(acc_full + a);
+              umma_ts_warp(tmem + a * kSub, tmem + kAcc * kSub + i * 64 + kk * 8,
+                           sw128_desc(qb + (kk >> 2) * C::kBoxQ + (kk & 3) * 32, 16, 1024), idesc, kk > 0 ? 1u : 0u, leader);
+            umma_commit_warp(acc_full + a, leader);
           }
-          if (ok) umma_commit(q_empty + s);
+          if (ok && (part == kQTile / kSub - 1 || n + 1 == n_sub)) {
+            umma_commit_warp(q_empty + s, leader);
+            ++n_done;
+          }
         }
         t += count;
       }
       if (!ok) {
-        atomicOr(p.status, kStatusTimeout);
+        if (leader) atomicOr(p.status, kStatusTimeout);
         *abort_flag = 1;
       }
-      umma_commit(final_bar);
-      mbar_wait(final_bar, 0, never);  // every MMA this thread issued has completed before TMEM is released
+      umma_commit_warp(final_bar, leader);
+      mbar_wait_warp(final_bar, 0, never);  // every MMA this thread issued has completed before TMEM is released
     }
   } else if (warp >= kFirstEpiWarp) {
-    // ------------------------------------------------------------------ key tiles into TMEM, sums
+    // ------------------------------------------------------------------ sums
     const int quarter = warp & 3;  // TMEM lane quarter this warp may access
     const int wg = (warp - kFirstEpiWarp) >> 2;
-    const int row = quarter * 32 + lane;  // key within the tile == TMEM lane
+    const int sel = wg & 1, half = wg >> 1;  // which accumulator, which 128 of its columns
+    const int row = quarter * 32 + lane;     // key within the tile == TMEM lane
     const int tid = wg * 128 + row;
     const uint32_t lane_addr = static_cast<uint32_t>(quarter * 32) << 16;
     const uint64_t sl2x2 = pack_f2(p.scale_log2, p.scale_log2);
@@ -222,25 +262,22 @@ __global__ void __launch_bounds__(kThreads, 1)
     int item = 0, seq0 = 0, staged_head = -1;
     for (int t = first; t < last; ++item) {
       const int count = tiles_at(p, t, last), head = t / p.tiles_per_head, key0 = (t % p.tiles_per_head) * kTile;
-      // Each warpgroup has drained its last accumulator of the item before, so with this barrier every
-      // product that read the key tiles in TMEM is complete.
-      asm volatile("bar.sync 1, 256;" ::: "memory");
+      // Every product of the item before is complete: the barrier at its end follows the last drains.
       if (alive) alive = mbar_wait_warp(k_full, item & 1, abort_flag);
-      if (alive && wg < count) {
+      if (alive && sel < count) {
         tc_fence_after();
-        const uint8_t* src = smem + C::kOffK + wg * C::kTileBytes + row * 128;
-#pragma unroll
-        for (int b = 0; b < C::kBoxes; ++b) {  // this key's 64 elements of a box: 16-byte chunk c sits at c ^ (row & 7)
+        const uint8_t* src = smem + C::kOffK + sel * C::kBytesK + row * 128;
+        for (int b = half; b < C::kBoxes; b += 2) {  // this key's 64 elements of a box: 16-byte chunk c sits at c ^ (row & 7)
           uint32_t r[32];
 #pragma unroll
           for (int c = 0; c < 8; ++c) {
-            const uint4 w = *reinterpret_cast<const uint4*>(src + b * C::kBoxBytes + ((c ^ (row & 7)) << 4));
+            const uint4 w = *reinterpret_cast<const uint4*>(src + b * C::kBoxK + ((c ^ (row & 7)) << 4));
             r[4 * c] = w.x;
             r[4 * c + 1] = w.y;
             r[4 * c + 2] = w.z;
             r[4 * c + 3] = w.w;
           }
-          tmem_st32(tmem + lane_addr + kAcc * kTile + wg * 64 + b * 32, r);
+          tmem_st32(tmem + lane_addr + kAcc * kSub + sel * 64 + b * 32, r);
         }
         tmem_wait_st();
         tc_fence_before();
@@ -254,44 +291,53 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int c0 = 0; c0 < p.n_q; c0 += kChunk) {
         const int c1 = min(p.n_q, c0 + kChunk);
         if (head != staged_head || p.n_q > kChunk) {  // -L of the chunk's queries; padding rows get weight 0
-          asm volatile("bar.sync 1, 256;" ::: "memory");
-          for (int i = tid; i < (c1 - c0 + kTile - 1) / kTile * kTile; i += 256) {
+          asm volatile("bar.sync 1, %0;" ::"n"(kEpiThreads) : "memory");
+          for (int i = tid; i < (c1 - c0 + kQTile - 1) / kQTile * kQTile; i += kEpiThreads) {
             const int64_t o = static_cast<int64_t>(head) * p.n_q + c0 + i;
             neg_l[i] = c0 + i < p.n_q ? -kLog2e * mass_row_lse(p.lse_loc[o], p.lse_hist ? p.lse_hist[o] : -INFINITY) : -INFINITY;
           }
-          asm volatile("bar.sync 1, 256;" ::: "memory");
+          asm volatile("bar.sync 1, %0;" ::"n"(kEpiThreads) : "memory");
           staged_head = head;
         }
-        for (int n = c0 / kTile; alive && n * kTile < c1; ++n) {
+        for (int n = c0 / kSub; alive && n * kSub < c1; ++n) {
           for (int i = 0; i < count; ++i) {
-            const int seq = seq0 + n * count + i;
-            if ((seq & 1) != wg) continue;
-            const int a = seq % kAcc;
+            const int seq = seq0 + n * count + i, a = seq % kAcc;
+            if ((seq & 1) != sel) continue;
             alive = mbar_wait_warp(acc_full + a, (seq / kAcc) & 1, abort_flag);
             if (!alive) break;
             tc_fence_after();
-            const float* nl = neg_l + n * kTile - c0;
+            const float* nl = neg_l + n * kSub - c0 + half * kCols;
+            uint32_t r[kCols];
+            const uint32_t src = tmem + lane_addr + a * kSub + half * kCols;
+#pragma unroll
+            for (int x = 0; x < kCols / 32; ++x) tmem_ld32(src + 32 * x, r + 32 * x);
+            tmem_wait_ld();
+            tc_fence_before();  // in registers: free the accumulator for the MMAs before any arithmetic
+            __syncwarp();
+            if (lane == 0) mbar_arrive(acc_empty + a);
+            const int cols = p.n_q - n * kSub - half * kCols;
+            if (cols < kCols) {  // columns past the last query hold what an earlier product left
+#pragma unroll
+              for (int j = 0; j < kCols; ++j)
+                if (j >= cols) r[j] = 0u;
+            }
             uint64_t acc[4] = {0ull, 0ull, 0ull, 0ull};
 #pragma unroll
-            for (int c = 0; c < kTile / 32; ++c) {
-              uint32_t r[32];
-              tmem_ld32(tmem + lane_addr + a * kTile + c * 32, r);
-              tmem_wait_ld();
-              if (c == kTile / 32 - 1) {  // the accumulator is in registers: free it for the MMAs
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(acc_empty + a);
-              }
+            for (int j = 0; j < kCols; j += 4) {
+              const float4 l4 = *reinterpret_cast<const float4*>(nl + j);
 #pragma unroll
-              for (int j = 0; j < 32; j += 4) {
-                const float4 l4 = *reinterpret_cast<const float4*>(nl + c * 32 + j);
-#pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                  const uint64_t y = fma_f2(pack_f2(__uint_as_float(r[j + 2 * h]), __uint_as_float(r[j + 2 * h + 1])), sl2x2,
-                                            h ? pack_f2(l4.z, l4.w) : pack_f2(l4.x, l4.y));
+              for (int h = 0; h < 2; ++h) {
+                const int pair = j >> 1 | h;
+                const uint64_t y = fma_f2(pack_f2(__uint_as_float(r[j + 2 * h]), __uint_as_float(r[j + 2 * h + 1])), sl2x2,
+                                          h ? pack_f2(l4.z, l4.w) : pack_f2(l4.x, l4.y));
+                if ((kPolyPairs >> (pair & 7)) & 1) {
+                  uint64_t pv, scale;
+                  exp2_poly2(y, pv, scale);
+                  acc[pair & 3] = fma_f2(pv, scale, acc[pair & 3]);
+                } else {
                   float y0, y1;
                   unpack_f2(y, y0, y1);
-                  acc[(j >> 1 | h) & 3] = add_f2(acc[(j >> 1 | h) & 3], pack_f2(fast_exp2(y0), fast_exp2(y1)));
+                  acc[pair & 3] = add_f2(acc[pair & 3], pack_f2(fast_exp2(y0), fast_exp2(y1)));
                 }
               }
             }
@@ -304,16 +350,20 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
       }
-      // With two tiles this warpgroup had the tile of its parity; with one, both worked on it.
-      const int mine = count == 2 ? wg ^ (seq0 & 1) : 0;
+      // With two tiles a warpgroup had the tile of its parity; with one, all four worked on it.  The sums
+      // are joined in a fixed order; the next item's may be written while these are read.
+      const int mine = count == 2 ? sel ^ (seq0 & 1) : 0;
       seq0 += n_sub * count;
-      if (count == 1) {
-        if (wg == 1) other[row] = total;
-        asm volatile("bar.sync 1, 256;" ::: "memory");
-        if (wg == 0) total += other[row];
+      float* sums = other + (item & 1) * 3 * kTile + row;
+      if (wg > 0) sums[(wg - 1) * kTile] = total;
+      asm volatile("bar.sync 1, %0;" ::"n"(kEpiThreads) : "memory");
+      const bool owner = half == 0 && (count == 2 || sel == 0);
+      if (owner) {
+        total += sums[(wg + 1) * kTile];
+        if (count == 1) total += sums[0] + sums[2 * kTile];
       }
       const int j = key0 + mine * kTile + row;
-      if (alive && (count == 2 || wg == 0) && j < p.n_k) {
+      if (alive && owner && j < p.n_k) {
         if (p.bias) total = mass_apply_bias(total, p.bias[static_cast<int64_t>(head) * p.ld_bias + j]);
         const int64_t o = static_cast<int64_t>(head) * p.ld_mass + j;
         p.mass_out[o] = p.decay != 0.f ? fmaf(p.decay, p.mass[o], total) : total;
@@ -339,7 +389,7 @@ cudaError_t launch_hd(const MassLaunch& a, cudaStream_t s, int* n_launched) {
   using C = Cfg<HD>;
   CUtensorMap map_q, map_k;
   const uint64_t d = static_cast<uint64_t>(a.n_heads) * HD;
-  if (!make_map_bf16_2d(&map_q, a.q, a.n_q, d, a.ld_q, 64, kTile) || !make_map_bf16_2d(&map_k, a.k, a.n_k, d, a.ld_k, 64, kTile))
+  if (!make_map_bf16_2d(&map_q, a.q, a.n_q, d, a.ld_q, 64, kQTile) || !make_map_bf16_2d(&map_k, a.k, a.n_k, d, a.ld_k, 64, kTile))
     return cudaErrorInvalidValue;
   Params p;
   p.n_q = static_cast<int>(a.n_q);
