@@ -102,7 +102,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_blocks_tc_kernel(const __gri
   int* n_halves_slot = reinterpret_cast<int*>(smem + C::kOffMisc + 12);
   int* list = reinterpret_cast<int*>(smem + C::kOffList);
 
-  const int warp = threadIdx.x >> 5;
+  const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0);  // warp-uniform
   const int lane = threadIdx.x & 31;
   const int head = blockIdx.y;
   const int q0 = blockIdx.x * kBM;
@@ -206,28 +206,29 @@ __global__ void __launch_bounds__(kThreads, 1) attn_blocks_tc_kernel(const __gri
     }
   } else if (warp == 1) {
     // ------------------------------------------------------------------ MMA issuer
-    if (lane == 0) {
-      bool ok = mbar_wait(q_full, 0, abort_flag);
+    {
+      const uint32_t leader = elect_leader();
+      bool ok = mbar_wait_warp(q_full, 0, abort_flag);
       tc_fence_after();
       const uint32_t q_base = smem_u32(smem + C::kOffQ);
       auto issue_pv = [&](int u) -> bool {
         const int b = u & 1;
-        if (!mbar_wait(p_ready + b, (u >> 1) & 1, abort_flag)) return false;
-        if (!mbar_wait(v_full + b, (u >> 1) & 1, abort_flag)) return false;
+        if (!mbar_wait_warp(p_ready + b, (u >> 1) & 1, abort_flag)) return false;
+        if (!mbar_wait_warp(v_full + b, (u >> 1) & 1, abort_flag)) return false;
         tc_fence_after();
         const uint32_t o_tmem = tmem + 256 + (u >= T1 ? HD : 0);
         const bool first = (u == 0) || (u == T1);
         const uint32_t v_base = smem_u32(smem + C::kOffV + b * C::kTileBytes);
 #pragma unroll
         for (int kk = 0; kk < kBN / 16; ++kk)
-          umma_ts(o_tmem, tmem + b * 128 + kk * 8, sw128_desc(v_base + kk * 16 * 128, C::kBoxBytes, 1024), C::kIdescPV,
-                  (!first || kk > 0) ? 1u : 0u);
-        umma_commit(o_done + b);
+          umma_ts_warp(o_tmem, tmem + b * 128 + kk * 8, sw128_desc(v_base + kk * 16 * 128, C::kBoxBytes, 1024), C::kIdescPV,
+                  (!first || kk > 0) ? 1u : 0u, leader);
+        umma_commit_warp(o_done + b, leader);
         return true;
       };
       for (int t = 0; ok && t < T; ++t) {
         const int s = t & 1;
-        if (!mbar_wait(k_full + s, (t >> 1) & 1, abort_flag)) {
+        if (!mbar_wait_warp(k_full + s, (t >> 1) & 1, abort_flag)) {
           ok = false;
           break;
         }
@@ -236,10 +237,10 @@ __global__ void __launch_bounds__(kThreads, 1) attn_blocks_tc_kernel(const __gri
 #pragma unroll
         for (int kk = 0; kk < HD / 16; ++kk) {
           const uint32_t off = (kk >> 2) * C::kBoxBytes + (kk & 3) * 32;
-          umma_ss(tmem + s * 128, sw128_desc(q_base + off, 16, 1024), sw128_desc(k_base + off, 16, 1024), C::kIdescQK,
-                  kk > 0 ? 1u : 0u);
+          umma_ss_warp(tmem + s * 128, sw128_desc(q_base + off, 16, 1024), sw128_desc(k_base + off, 16, 1024), C::kIdescQK,
+                  kk > 0 ? 1u : 0u, leader);
         }
-        umma_commit(s_full + s);
+        umma_commit_warp(s_full + s, leader);
         if (t > 0 && !issue_pv(t - 1)) {
           ok = false;
           break;
@@ -247,12 +248,12 @@ __global__ void __launch_bounds__(kThreads, 1) attn_blocks_tc_kernel(const __gri
       }
       if (ok && T > 0) ok = issue_pv(T - 1);
       if (!ok) {
-        atomicOr(p.status, kStatusTimeout);
+        if (leader) atomicOr(p.status, kStatusTimeout);
         *abort_flag = 1;
       }
-      umma_commit(o_final);
-      umma_commit(final_bar);
-      mbar_wait(final_bar, 0, never);  // every MMA this thread issued has completed before TMEM is released
+      umma_commit_warp(o_final, leader);
+      umma_commit_warp(final_bar, leader);
+      mbar_wait_warp(final_bar, 0, never);  // every MMA this thread issued has completed before TMEM is released
     }
   } else {
     // ------------------------------------------------------------------ softmax + epilogue

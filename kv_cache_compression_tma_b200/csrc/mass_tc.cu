@@ -49,7 +49,8 @@ constexpr int kFirstEpiWarp = 3;
 constexpr int kEpiThreads = 512;
 constexpr int kThreads = 32 * kFirstEpiWarp + kEpiThreads;
 // Of eight pairs of queries, those whose exponentials run on the multiply-add pipes, the others on the
-// special-function unit: it alone takes 16 a clock, less than the products deliver.
+// special-function unit: it alone takes 16 a clock, less than the products deliver.  (No exponent passes
+// 127: a key that counts has no weight above exp(-bias) <= e^64.)
 constexpr int kPolyPairs = 0b10001000;
 constexpr float kLog2e = 1.4426950408889634f;
 
@@ -81,30 +82,6 @@ struct Cfg {
   static constexpr int kSmemBytes = kOffMisc + 16 + 2 * 3 * kTile * 4;  // and the warpgroups' sums of an item, by its parity
   static_assert(kSmemBytes <= 232448, "shared memory budget");
 };
-
-// 2^y of a pair, by the fused multiply-add pipes: n = round(y), a polynomial of degree 4 for 2^(y - n) on
-// [-1/2, 1/2] (weighted least squares iterated to equal ripple: largest relative error 2.7e-6, mean
-// 4e-8, so a sum of many loses nothing), and 2^n from n's bits.  Returns the polynomial's value and
-// 2^n apart: the caller's accumulation multiplies them.  y below -127 gives n = -127, whose 2^n is 0;
-// NaN stays NaN.
-__device__ __forceinline__ void exp2_poly2(uint64_t y, uint64_t& p, uint64_t& scale) {
-  float y0, y1;
-  unpack_f2(y, y0, y1);
-  asm("max.NaN.f32 %0, %0, %1;" : "+f"(y0) : "f"(-127.f));
-  asm("max.NaN.f32 %0, %0, %1;" : "+f"(y1) : "f"(-127.f));
-  const uint64_t yc = pack_f2(y0, y1);
-  const uint64_t magic = pack_f2(12582912.f, 12582912.f);  // 1.5 * 2^23: the sum's low mantissa bits are n
-  const uint64_t t = add_f2(yc, magic);
-  const uint64_t n = add_f2(t, pack_f2(-12582912.f, -12582912.f));
-  const uint64_t f = fma_f2(n, pack_f2(-1.f, -1.f), yc);
-  p = fma_f2(pack_f2(9.570102207362652e-3f, 9.570102207362652e-3f), f, pack_f2(5.591785907745361e-2f, 5.591785907745361e-2f));
-  p = fma_f2(p, f, pack_f2(2.40247443318367e-1f, 2.40247443318367e-1f));
-  p = fma_f2(p, f, pack_f2(6.931217908859253e-1f, 6.931217908859253e-1f));
-  p = fma_f2(p, f, pack_f2(9.999992847442627e-1f, 9.999992847442627e-1f));
-  float t0, t1;
-  unpack_f2(t, t0, t1);
-  scale = pack_f2(__uint_as_float((__float_as_uint(t0) << 23) + 0x3f800000u), __uint_as_float((__float_as_uint(t1) << 23) + 0x3f800000u));
-}
 
 // The CTA's tiles [first, last) one or two at a time: two only within a head.
 __device__ __forceinline__ int tiles_at(const Params& p, int t, int last) {
