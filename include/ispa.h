@@ -326,7 +326,7 @@ ISPA_API ispa_status ispa_tempcache_merge(int32_t n_heads, int32_t head_dim, voi
  * ISPA_BF16: head_dim 64 or 128, else ISPA_ERR_UNSUPPORTED unless flags has ISPA_ATTN_CUDA_CORES, which
  * admits 16 and 32 too.  ISPA_F32: head_dim 16, 32, 64 or 128, on CUDA cores.  Any alignment; bf16
  * keys and queries at 16-byte aligned addresses with strides that are multiples of 8 run on the tensor
- * cores when there are enough queries.  Deterministic.  n_k == 0 is a no-op; n_q == 0 only decays.
+ * cores.  Deterministic.  n_k == 0 is a no-op; n_q == 0 only decays.
  */
 ISPA_API ispa_status ispa_attn_mass(int32_t dtype, int32_t n_heads, int32_t head_dim, const void* q, int64_t n_q,
                                     int64_t ld_q, const void* k, int64_t n_k, int64_t ld_k, const float* lse_loc,
@@ -397,9 +397,9 @@ ISPA_API ispa_status ispa_block_select(int32_t dtype, int32_t n_heads, int32_t h
  *   D = 0.  n_sel == 0 (idx unused) is attention over sink and local alone.
  * Every entry of idx is read on the device when the kernel runs.  ISPA_BF16 with q_block a multiple of
  * 128 runs on the tensor cores (block 64 or 128, n_sel <= 4096, head_dim 64 or 128 and the alignment rules
- * of ispa_dual_stream_attn, else ISPA_ERR_UNSUPPORTED), ISPA_BF16 with q_block 1 (each query its own
- * picks: the single-token form) on CUDA cores at any alignment; another q_block is
- * ISPA_ERR_UNSUPPORTED.  ISPA_F32, or ISPA_BF16 with ISPA_ATTN_CUDA_CORES, runs on CUDA cores with any
+ * of ispa_dual_stream_attn, else ISPA_ERR_UNSUPPORTED; calls of few rows take the row kernel there too),
+ * ISPA_BF16 with q_block 1 (each query its own picks: the single-token form) on the row kernel, at any
+ * alignment; another q_block is ISPA_ERR_UNSUPPORTED.  ISPA_F32, or ISPA_BF16 with ISPA_ATTN_CUDA_CORES, runs on CUDA cores with any
  * q_block >= 1, block of 1 to 65536, head_dim 16, 32, 64 or 128 and any alignment.
  */
 ISPA_API ispa_status ispa_block_sparse_attn(const ispa_attn_args* args, const int32_t* idx, int32_t n_sel,

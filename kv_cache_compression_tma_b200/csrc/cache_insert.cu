@@ -31,6 +31,7 @@ constexpr int kMaxCluster = 16;
 constexpr int kMaxCached = 32768;   // order keys per CTA held in shared memory (128 KB)
 constexpr int kMaxNewSlice = 4096;  // new tokens per CTA: their list of slots and of sources (32 KB)
 constexpr int kUnroll = 16;         // state words in flight per thread while the keys are formed
+constexpr int kRun = 8;             // consecutive candidates of a lane where ranks are counted
 constexpr int kShort = 2048;        // candidates sharing the first digit that are listed apart
 
 struct Shared {
@@ -95,14 +96,15 @@ __global__ void __launch_bounds__(kThreads) cache_insert_kernel(const InsertLaun
     return order_key(mass_new ? mass_new[t] : 0.f, a.pos_new + t, a.keep_below, a.keep_from);
   };
   auto key_at = [&](int i) -> uint32_t { return cached ? keys[i] : make_key(i); };
-  // Four consecutive candidates of the held slice from i (a multiple of 4) on, as `none` past the slice.
-  auto four_keys = [&](int i, uint32_t none, uint32_t* k) {
-    if (cached && i + 3 < old_n) {
-      const uint4 w = *reinterpret_cast<const uint4*>(keys + i);
-      k[0] = w.x, k[1] = w.y, k[2] = w.z, k[3] = w.w;
+  // kRun consecutive candidates of the held slice from i (a multiple of kRun) on, all ones past the slice (no
+  // key is: NaN ranks as -inf).
+  auto key_run = [&](int i, uint32_t* k) {
+    if (cached && i + kRun <= old_n) {
+#pragma unroll
+      for (int x = 0; x < kRun; x += 4) *reinterpret_cast<uint4*>(k + x) = *reinterpret_cast<const uint4*>(keys + i + x);
     } else {
 #pragma unroll
-      for (int x = 0; x < 4; ++x) k[x] = i + x < old_n ? key_at(i + x) : none;
+      for (int x = 0; x < kRun; ++x) k[x] = i + x < old_n ? key_at(i + x) : 0xffffffffu;
     }
   };
 
@@ -217,16 +219,16 @@ __global__ void __launch_bounds__(kThreads) cache_insert_kernel(const InsertLaun
 
   // Counts of candidates below and at the threshold: per warp over contiguous pieces, so that ranks
   // follow the candidate order.
-  const int old_w = (old_n + 128 * kWarps - 1) / (128 * kWarps) * 128, new_w = (new_n + kWarps - 1) / kWarps;
+  const int old_w = (old_n + 32 * kRun * kWarps - 1) / (32 * kRun * kWarps) * 32 * kRun, new_w = (new_n + kWarps - 1) / kWarps;
   const int oa = min(old_n, warp * old_w), ob = min(old_n, oa + old_w);
   const int na = old_n + min(new_n, warp * new_w), nb = min(all, na + new_w);
   if (drop > 0) {
     uint32_t c[4] = {};
-    for (int i = oa + 4 * lane; i < ob; i += 128) {
-      uint32_t k[4];
-      four_keys(i, 0xffffffffu, k);  // no key is all ones (NaN ranks as -inf)
+    for (int i = oa + kRun * lane; i < ob; i += 32 * kRun) {
+      uint32_t k[kRun];
+      key_run(i, k);
 #pragma unroll
-      for (int x = 0; x < 4; ++x) {
+      for (int x = 0; x < kRun; ++x) {
         c[0] += k[x] < threshold;
         c[1] += k[x] == threshold;
       }
@@ -285,35 +287,30 @@ __global__ void __launch_bounds__(kThreads) cache_insert_kernel(const InsertLaun
   const uint32_t lt = (1u << lane) - 1u;
   if (drop > 0) {
     // evicted held entries: slot of hole rank r goes to the CTA that owns survivor r
-    for (int i = oa; i < ob; i += 128) {  // four consecutive entries a lane
-      uint32_t k[4];
-      four_keys(i + 4 * lane, 0xffffffffu, k);
-      bool out[4], any = false;
-      uint32_t eq = 0;
+    for (int i = oa; i < ob; i += 32 * kRun) {
+      uint32_t k[kRun];
+      key_run(i + kRun * lane, k);
+      uint32_t out = 0, eq = 0;  // bit x: candidate x leaves, equals the threshold
 #pragma unroll
-      for (int x = 0; x < 4; ++x) {
-        out[x] = k[x] < threshold;
-        eq += k[x] == threshold;
-        any = any || k[x] <= threshold;
+      for (int x = 0; x < kRun; ++x) {
+        out |= (k[x] < threshold ? 1u : 0u) << x;
+        eq |= (k[x] == threshold ? 1u : 0u) << x;
       }
-      if (!__any_sync(0xffffffffu, any)) continue;
-      if (__any_sync(0xffffffffu, eq > 0)) {
-        uint32_t e = eq_o + warp_before(eq, lane);
-#pragma unroll
-        for (int x = 0; x < 4; ++x)
-          if (k[x] == threshold) out[x] = e++ >= stay_equal;
-        eq_o += __reduce_add_sync(0xffffffffu, eq);
+      if (!__any_sync(0xffffffffu, out | eq)) continue;
+      if (__any_sync(0xffffffffu, eq)) {
+        const uint32_t n_eq = __popc(eq);
+        uint32_t e = eq_o + warp_before(n_eq, lane);
+        for (uint32_t w = eq; w; w &= w - 1)
+          if (e++ >= stay_equal) out |= w & -w;
+        eq_o += __reduce_add_sync(0xffffffffu, n_eq);
       }
-      const uint32_t n_out = out[0] + out[1] + out[2] + out[3];
+      const uint32_t n_out = __popc(out);
       uint32_t r = hole + warp_before(n_out, lane);
-#pragma unroll
-      for (int x = 0; x < 4; ++x)
-        if (out[x]) {
-          int owner = 0;
-          while (r >= sh.first_survivor[owner + 1]) ++owner;  // r < survivors of the head: one leaves per hole
-          cluster.map_shared_rank(slot_of, owner)[r - sh.first_survivor[owner]] = old0 + i + 4 * lane + x;
-          ++r;
-        }
+      int owner = 0;
+      for (; out; out &= out - 1, ++r) {
+        while (r >= sh.first_survivor[owner + 1]) ++owner;  // r < survivors of the head: one leaves per hole
+        cluster.map_shared_rank(slot_of, owner)[r - sh.first_survivor[owner]] = old0 + i + kRun * lane + __ffs(out) - 1;
+      }
       hole += __reduce_add_sync(0xffffffffu, n_out);
     }
   }
@@ -367,6 +364,70 @@ __global__ void __launch_bounds__(kThreads) cache_insert_kernel(const InsertLaun
   }
 }
 
+// One new token (a decoding step): at most one candidate leaves, the one of lowest rank (the last of
+// equals), so one CTA per head takes a minimum over its candidates instead of a radix select: 17 -> 6 us
+// for 40 heads of 14040 entries.
+__global__ void __launch_bounds__(kThreads) cache_insert_one_kernel(const InsertLaunch a, int unit) {
+  __shared__ unsigned long long lowest[kWarps];
+  const int head = blockIdx.x, tid = threadIdx.x, lane = tid & 31;
+  const float* mass = a.mass + static_cast<int64_t>(head) * a.ld_state;
+  const int32_t* pos = a.pos + static_cast<int64_t>(head) * a.ld_state;
+  float* mass_out = a.mass_out + static_cast<int64_t>(head) * a.ld_out;
+  int32_t* pos_out = a.pos_out + static_cast<int64_t>(head) * a.ld_out;
+  const float m_new = a.mass_new ? a.mass_new[static_cast<int64_t>(head) * a.ld_new_state] : 0.f;
+  const bool full = a.n == a.capacity;
+  const bool copy_mass = a.mass_out != a.mass, copy_pos = a.pos_out != a.pos;
+  // (order key, candidate counted from the end): the least pair leaves
+  auto pair = [&](float m, int32_t p, int i) {
+    return static_cast<unsigned long long>(order_key(m, p, a.keep_below, a.keep_from)) << 32 | static_cast<uint32_t>(a.n - i);
+  };
+  unsigned long long least = pair(m_new, a.pos_new, a.n);
+  if (full || copy_mass || copy_pos) {
+    for (int i0 = tid; i0 < a.n; i0 += kUnroll * kThreads) {
+      float m[kUnroll];
+      int32_t q[kUnroll];
+#pragma unroll
+      for (int u = 0; u < kUnroll; ++u) {
+        const int i = min(i0 + u * kThreads, a.n - 1);
+        m[u] = mass[i];
+        q[u] = pos[i];
+      }
+#pragma unroll
+      for (int u = 0; u < kUnroll; ++u) {
+        const int i = i0 + u * kThreads;
+        if (i >= a.n) break;
+        least = min(least, pair(m[u], q[u], i));
+        if (copy_mass) mass_out[i] = m[u];
+        if (copy_pos) pos_out[i] = q[u];
+      }
+    }
+  }
+#pragma unroll
+  for (int off = 16; off > 0; off >>= 1) least = min(least, __shfl_xor_sync(0xffffffffu, least, off));
+  if (lane == 0) lowest[tid >> 5] = least;
+  __syncthreads();  // also: every read of the state is done before its slot is written
+  if (tid >= 32) return;
+  least = lowest[lane];
+#pragma unroll
+  for (int off = 16; off > 0; off >>= 1) least = min(least, __shfl_xor_sync(0xffffffffu, least, off));
+  const int slot = full ? a.n - static_cast<int>(static_cast<uint32_t>(least)) : a.n;
+  if (slot == a.capacity) return;  // the token itself leaves
+  if (lane == 0) {
+    mass_out[slot] = m_new;
+    pos_out[slot] = a.pos_new;
+  }
+  const int64_t col = static_cast<int64_t>(head) * a.row_bytes;
+  const uint8_t* src = static_cast<const uint8_t*>(lane < 16 ? a.k_new : a.v_new) + col;
+  uint8_t* dst = static_cast<uint8_t*>(lane < 16 ? a.k : a.v) + slot * a.ld_cache_bytes + col;
+  if (unit == 16) {
+    for (int b = (lane & 15) * 16; b < a.row_bytes; b += 256)
+      *reinterpret_cast<uint4*>(dst + b) = __ldg(reinterpret_cast<const uint4*>(src + b));
+  } else {
+    for (int b = (lane & 15) * 2; b < a.row_bytes; b += 32)
+      *reinterpret_cast<uint16_t*>(dst + b) = __ldg(reinterpret_cast<const uint16_t*>(src + b));
+  }
+}
+
 }  // namespace
 
 bool cache_insert_supported(int64_t n, int64_t n_new) {
@@ -374,6 +435,14 @@ bool cache_insert_supported(int64_t n, int64_t n_new) {
 }
 
 cudaError_t launch_cache_insert(const InsertLaunch& a, cudaStream_t s, int* n_launched) {
+  const bool al = aligned16(a.k) && aligned16(a.v) && aligned16(a.k_new) && aligned16(a.v_new) &&
+                  a.ld_cache_bytes % 16 == 0 && a.ld_new_bytes % 16 == 0 && a.row_bytes % 16 == 0;
+  const int unit = al ? 16 : 2;
+  if (a.n_new == 1) {
+    cache_insert_one_kernel<<<static_cast<unsigned>(a.n_heads), kThreads, 0, s>>>(a, unit);
+    *n_launched += 1;
+    return cudaGetLastError();
+  }
   // Cluster size: a CTA (one per SM: 1024 threads) forms and searches about 16 thousand order keys in the
   // time of the cluster barriers, so a head is split only beyond that, and only while all clusters
   // can run at once (clusters of 16 fit 8 times on the GPU's 8 GPCs of 16 to 20 SMs, of 8 twice as often).
@@ -384,8 +453,6 @@ cudaError_t launch_cache_insert(const InsertLaunch& a, cudaStream_t s, int* n_la
   const int old_per = (a.n + C - 1) / C, new_per = (a.n_new + C - 1) / C;
   const int cached = old_per + new_per <= kMaxCached;
   const size_t smem = 4ull * ((cached ? old_per + new_per : 0) + 2ll * new_per);
-  const bool al = aligned16(a.k) && aligned16(a.v) && aligned16(a.k_new) && aligned16(a.v_new) &&
-                  a.ld_cache_bytes % 16 == 0 && a.ld_new_bytes % 16 == 0 && a.row_bytes % 16 == 0;
   cudaError_t e = cudaFuncSetAttribute(cache_insert_kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
   if (e == cudaSuccess)
     e = cudaFuncSetAttribute(cache_insert_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
@@ -403,7 +470,7 @@ cudaError_t launch_cache_insert(const InsertLaunch& a, cudaStream_t s, int* n_la
   attr[0].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  e = cudaLaunchKernelEx(&cfg, cache_insert_kernel, a, cached, al ? 16 : 2);
+  e = cudaLaunchKernelEx(&cfg, cache_insert_kernel, a, cached, unit);
   *n_launched += 1;
   return e != cudaSuccess ? e : cudaGetLastError();
 }

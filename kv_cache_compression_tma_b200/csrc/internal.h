@@ -231,7 +231,8 @@ struct MassLaunch {
 // tcgen05 kernel: bf16, head_dim 64 or 128, TMA-compatible strides, at least one query
 bool mass_tc_supported(const MassLaunch& a);
 cudaError_t launch_mass_tc(const MassLaunch& a, cudaStream_t s, int* n_launched);
-// CUDA cores, any case
+// any case; bf16 calls of up to kMassFewQueries queries over aligned keys read them at the memory's rate
+constexpr int64_t kMassFewQueries = 32;
 cudaError_t launch_mass_rows(const MassLaunch& a, cudaStream_t s, int* n_launched);
 
 // ------------------------------------------------------------------ cache insertion with eviction

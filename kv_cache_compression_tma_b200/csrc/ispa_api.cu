@@ -47,8 +47,10 @@ void count(int n) { g_launches.fetch_add(static_cast<uint64_t>(n)); }
 
 bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
 
-// Up to this many queries the row kernel of ispa_attn_mass reads the keys at the memory's rate.
-constexpr int64_t kMassRowsMaxQueries = 8;
+// Up to this many (query, head) rows, block-sparse attention of whole row groups takes the row kernel:
+// 80 rows of 40 heads 46 us against 65 on the tensor cores, 96 of 12 heads 73 against 103, but 160 of
+// 40 heads 89 against 65 (each row reads its keys for itself).
+constexpr int64_t kBlockRowsMax = 96;
 
 // head dimensions of the kernels that spread a head's row over lanes
 bool rows_head_dim(int32_t hd) { return hd == 16 || hd == 32 || hd == 64 || hd == 128; }
@@ -439,7 +441,7 @@ ispa_status ispa_attn_mass(int32_t dtype, int32_t n_heads, int32_t head_dim, con
   if (!L.status) return ISPA_ERR_CUDA;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   int n = 0;
-  const bool tc = !cuda_cores && n_q > kMassRowsMaxQueries && mass_tc_supported(L);
+  const bool tc = !cuda_cores && n_q > kMassFewQueries && mass_tc_supported(L);
   cudaError_t e = tc ? launch_mass_tc(L, st, &n) : launch_mass_rows(L, st, &n);
   count(n);
   return e == cudaSuccess ? ISPA_OK : ISPA_ERR_CUDA;
@@ -533,8 +535,9 @@ ispa_status ispa_block_sparse_attn(const ispa_attn_args* a, const int32_t* idx, 
   const BlockList B{idx, n_sel, block, q_block, (a->n_q + q_block - 1) / q_block,
                     static_cast<int>((a->n_kv[ISPA_SEG_HIST] + block - 1) / block)};
   // bf16 groups of rows run on the tensor cores or not at all, unless the caller asks for CUDA cores
-  const bool rows = cuda_cores || q_block == 1;
-  if (!rows && !attn_blocks_tc_supported(L, B)) return ISPA_ERR_UNSUPPORTED;
+  const bool groups = !cuda_cores && q_block != 1;
+  if (groups && !attn_blocks_tc_supported(L, B)) return ISPA_ERR_UNSUPPORTED;
+  const bool rows = !groups || a->n_q * a->n_heads <= kBlockRowsMax;
   if (a->n_q == 0) return ISPA_OK;
   L.status = status_ptr();
   if (!L.status) return ISPA_ERR_CUDA;

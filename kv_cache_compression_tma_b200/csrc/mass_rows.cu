@@ -4,7 +4,7 @@
 //   L_i = log(exp(lse_loc_i) + exp(lse_hist_i)),
 // for few queries (single-token steps, bf16) and for every fp32 call.  K is read once whatever n_q is.
 //
-// Up to 8 bf16 queries: a warp takes 16 keys at a time, their rows go from memory straight into the
+// Up to 32 bf16 queries: a warp takes 16 keys at a time, their rows go from memory straight into the
 // fragments of mma.m16n8k16 (8 query columns cost the same as one), and the next 16 keys are loaded
 // while the present ones are worked on.  Bound by the read of K: the same sums by multiply-adds and
 // shuffles took 53 instructions a key and issue, not memory, set the pace.
@@ -31,50 +31,66 @@ constexpr int kRows = 4;    // keys per lane group and step: 4 independent 16-by
 constexpr int kSteps = 4;   // steps per CTA (few queries)
 constexpr int kQTile = 32;  // queries staged at a time
 
-// ---------------------------------------------------------------- up to 8 bf16 queries
-template <int HD>
+// ---------------------------------------------------------------- up to 32 bf16 queries
+// kCols: groups of 8 queries (1, 2 or 4); one group's fragments stay in registers, more in shared memory.
+template <int HD, int kCols>
 __global__ void __launch_bounds__(kThreads, 2) mass_few_kernel(const MassLaunch a, int ctas_per_head) {
   using M = Mma16<HD>;
+  __shared__ uint4 sq[kCols > 1 ? kCols * M::kPieces : 1][32];  // [group, piece][lane]
   const int head = static_cast<int>(blockIdx.x % a.n_heads);  // heads first: CTAs that run together share rows
   const int cta = static_cast<int>(blockIdx.x / a.n_heads);
-  const int warp = threadIdx.x >> 5, g = (threadIdx.x & 31) >> 2, c = threadIdx.x & 3;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
   const auto* K = static_cast<const __nv_bfloat16*>(a.k) + static_cast<int64_t>(head) * HD + 8 * c;
   const auto* Q = static_cast<const __nv_bfloat16*>(a.q) + static_cast<int64_t>(head) * HD + 8 * c;
   const int64_t units = (a.n_k + 15) / 16, stride = static_cast<int64_t>(ctas_per_head) * kWarps;
   int64_t u = static_cast<int64_t>(cta) * kWarps + warp;
-  if (u >= units) return;
   auto load = [&](int64_t unit, M& m) {  // rows past the end repeat the last key
     m.load(K + min(unit * 16 + g, a.n_k - 1) * a.ld_k, K + min(unit * 16 + g + 8, a.n_k - 1) * a.ld_k);
   };
   M cur, next;
-  load(u, cur);
+  if (u < units) load(u, cur);
+  auto piece = [&](int col, int j) {
+    const int i = col * 8 + g;
+    return i < a.n_q ? load_raw<__nv_bfloat16, false>(Q + i * a.ld_q + 32 * j) : make_uint4(0, 0, 0, 0);
+  };
   uint4 q[M::kPieces];
+  if constexpr (kCols == 1) {
 #pragma unroll
-  for (int j = 0; j < M::kPieces; ++j)
-    q[j] = g < a.n_q ? load_raw<__nv_bfloat16, false>(Q + g * a.ld_q + 32 * j) : make_uint4(0, 0, 0, 0);
-  // this lane's two query columns
+    for (int j = 0; j < M::kPieces; ++j) q[j] = piece(0, j);
+  } else {
+    for (int x = warp; x < kCols * M::kPieces; x += kWarps) sq[x][lane] = piece(x / M::kPieces, x % M::kPieces);
+    __syncthreads();
+  }
+  // this lane's two query columns of each group; a column without a query, or a row without keys, adds 0
   constexpr float kLog2e = 1.4426950408889634f;
   const float sl2 = a.scale * kLog2e;
-  bool live[2];
-  float nl[2];
+  float nl[kCols][2];
 #pragma unroll
-  for (int x = 0; x < 2; ++x) {
-    const int i = 2 * c + x;
-    live[x] = i < a.n_q;
-    const int64_t o = static_cast<int64_t>(head) * a.n_q + (live[x] ? i : 0);
-    nl[x] = -kLog2e * mass_row_lse(a.lse_loc[o], a.lse_hist ? a.lse_hist[o] : -INFINITY);
-  }
+  for (int col = 0; col < kCols; ++col)
+#pragma unroll
+    for (int x = 0; x < 2; ++x) {
+      const int i = col * 8 + 2 * c + x;
+      const int64_t o = static_cast<int64_t>(head) * a.n_q + i;
+      nl[col][x] = i < a.n_q ? -kLog2e * mass_row_lse(a.lse_loc[o], a.lse_hist ? a.lse_hist[o] : -INFINITY) : -INFINITY;
+    }
   for (; u < units; u += stride) {
     if (u + stride < units) load(u + stride, next);
-    float d[4];
-    cur.scores(q, d);
     float lo = 0.f, hi = 0.f;
 #pragma unroll
-    for (int x = 0; x < 2; ++x)
-      if (live[x]) {
-        lo += fast_exp2(fmaf(d[x], sl2, nl[x]));
-        hi += fast_exp2(fmaf(d[2 + x], sl2, nl[x]));
+    for (int col = 0; col < kCols; ++col) {
+      if constexpr (kCols > 1) {
+#pragma unroll
+        for (int j = 0; j < M::kPieces; ++j) q[j] = sq[col * M::kPieces + j][lane];
       }
+      float d[4];
+      cur.scores(q, d);
+#pragma unroll
+      for (int x = 0; x < 2; ++x) {
+        const bool live = nl[col][x] > -INFINITY || nl[col][x] != nl[col][x];  // a NaN stays one
+        lo += live ? fast_exp2(fmaf(d[x], sl2, nl[col][x])) : 0.f;
+        hi += live ? fast_exp2(fmaf(d[2 + x], sl2, nl[col][x])) : 0.f;
+      }
+    }
     lo = row_sum<4>(lo);
     hi = row_sum<4>(hi);
     const int64_t j = u * 16 + g + 8 * c;
@@ -94,7 +110,13 @@ cudaError_t launch_few(const MassLaunch& a, cudaStream_t s, int* n) {
   const int64_t units = (a.n_k + 15) / 16;
   const int64_t per_head = 296 / a.n_heads > 0 ? 296 / a.n_heads : 1;
   const int ctas = static_cast<int>(std::min(per_head, (units + kWarps - 1) / kWarps));
-  mass_few_kernel<HD><<<static_cast<unsigned>(ctas) * static_cast<unsigned>(a.n_heads), kThreads, 0, s>>>(a, ctas);
+  const unsigned grid = static_cast<unsigned>(ctas) * static_cast<unsigned>(a.n_heads);
+  if (a.n_q <= 8)
+    mass_few_kernel<HD, 1><<<grid, kThreads, 0, s>>>(a, ctas);
+  else if (a.n_q <= 16)
+    mass_few_kernel<HD, 2><<<grid, kThreads, 0, s>>>(a, ctas);
+  else
+    mass_few_kernel<HD, 4><<<grid, kThreads, 0, s>>>(a, ctas);
   *n += 1;
   return cudaGetLastError();
 }
@@ -230,7 +252,7 @@ cudaError_t launch_t(const MassLaunch& a, cudaStream_t s, int* n) {
 }  // namespace
 
 cudaError_t launch_mass_rows(const MassLaunch& a, cudaStream_t s, int* n_launched) {
-  if (a.dtype == 0 && a.n_q >= 1 && a.n_q <= 8 && (a.head_dim == 64 || a.head_dim == 128) && aligned16(a.k) && a.ld_k % 8 == 0)
+  if (a.dtype == 0 && a.n_q >= 1 && a.n_q <= kMassFewQueries && (a.head_dim == 64 || a.head_dim == 128) && aligned16(a.k) && a.ld_k % 8 == 0)
     return a.head_dim == 128 ? launch_few<128>(a, s, n_launched) : launch_few<64>(a, s, n_launched);
   return a.dtype == 1 ? launch_t<float>(a, s, n_launched) : launch_t<__nv_bfloat16>(a, s, n_launched);
 }

@@ -73,6 +73,7 @@ def check_mass(q, k, ll, lh, mass, decay, bias=None, **kw):
 
 @pytest.mark.parametrize("dtype,hd,n_q,n_k,H", [
     ("bf16", 128, 1, 1, 1), ("bf16", 128, 1, 1000, 3), ("bf16", 64, 3, 257, 2), ("bf16", 128, 17, 129, 2),
+    ("bf16", 64, 9, 130, 3), ("bf16", 128, 32, 100, 2), ("bf16", 128, 33, 100, 2),
     ("bf16", 128, 128, 256, 2), ("bf16", 64, 129, 255, 2), ("bf16", 128, 300, 700, 2), ("bf16", 64, 513, 130, 1),
     ("fp32", 16, 5, 70, 3), ("fp32", 32, 64, 96, 2), ("fp32", 64, 33, 31, 2), ("fp32", 128, 2, 300, 2),
 ])
@@ -114,7 +115,7 @@ def test_mass_many_tiles_and_query_chunks(cuda_ok, H, n_q, n_k, hd):
     assert ((mass.double() - want).abs() / want).max().item() <= MASS_TOL
 
 
-@pytest.mark.parametrize("n_q", [2, 200])
+@pytest.mark.parametrize("n_q", [2, 20, 200])
 def test_mass_rows_without_keys_masked_nan_and_decay_zero(cuda_ok, n_q):
     """Rows with both lse's -inf add nothing; an excluded key's NaN stays out; decay 0 does not read the
     old mass (NaN there); no history branch; strided and (CUDA cores) unaligned operands."""
@@ -186,7 +187,7 @@ def check_insert(cap, n, n_new, H, hd, dtype, seed, below=0, frm=None, pad=0, le
 
 
 @pytest.mark.parametrize("cap,n,n_new,H,hd,dtype", [
-    (1, 1, 1, 1, 16, "fp32"), (1, 0, 3, 2, 64, "bf16"), (8, 0, 5, 2, 64, "bf16"), (100, 100, 1, 3, 128, "bf16"),
+    (1, 1, 1, 1, 16, "fp32"), (1, 0, 1, 2, 64, "bf16"), (7, 5, 1, 2, 64, "bf16"), (20001, 20001, 1, 2, 32, "bf16"), (1, 0, 3, 2, 64, "bf16"), (8, 0, 5, 2, 64, "bf16"), (100, 100, 1, 3, 128, "bf16"),
     (100, 97, 10, 3, 128, "bf16"), (64, 64, 200, 2, 64, "bf16"), (1025, 1025, 700, 2, 32, "bf16"),
     (5000, 5000, 1300, 2, 64, "bf16"), (20000, 19990, 321, 1, 16, "bf16"), (333, 333, 333, 2, 32, "fp32"),
 ])
@@ -196,7 +197,7 @@ def test_insert(cuda_ok, cap, n, n_new, H, hd, dtype, separate):
 
 
 def test_insert_ties_nan_protection_and_layouts(cuda_ok):
-    for cap, n, n_new in ((60, 60, 25), (3000, 2990, 900)):
+    for cap, n, n_new in ((60, 60, 25), (3000, 2990, 900), (50, 50, 1), (3000, 3000, 1)):
         check_insert(cap, n, n_new, 2, 64, "bf16", 20, ties=True)
         check_insert(cap, n, n_new, 2, 64, "bf16", 21, below=cap // 4, frm=n_new // 2, ties=True, separate=True)
         check_insert(cap, n, n_new, 2, 64, "bf16", 22, frm=n_new, pad=8)            # every new token protected
@@ -322,7 +323,7 @@ def test_sparse_rows_fp32(cuda_ok, H, hd, n_q, q_block, n_sink, n_loc, n_hist, b
 @pytest.mark.parametrize("H,hd,n_q,q_block,n_sink,n_loc,n_hist,block,n_sel", [
     (1, 64, 1, 128, 0, 1, 1, 64, 1), (2, 128, 300, 128, 40, 300, 1000, 64, 5), (2, 128, 257, 128, 0, 130, 777, 128, 3),
     (2, 64, 128, 128, 10, 0, 300, 64, 9), (1, 128, 700, 256, 128, 256, 4000, 128, 33), (3, 64, 130, 384, 1, 1, 63, 128, 2),
-    (1, 128, 129, 128, 0, 64, 192, 128, 2),
+    (1, 128, 129, 128, 0, 64, 192, 128, 2), (2, 128, 48, 128, 5, 64, 192, 64, 2), (2, 128, 49, 128, 5, 64, 192, 64, 2),
 ])
 @pytest.mark.parametrize("pad", [0, 8])
 def test_sparse_tensor_cores(cuda_ok, H, hd, n_q, q_block, n_sink, n_loc, n_hist, block, n_sel, pad):
