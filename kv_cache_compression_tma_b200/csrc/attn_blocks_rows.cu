@@ -166,7 +166,7 @@ __global__ void __launch_bounds__(Kind<T, HD, kAligned>::kThreads, Kind<T, HD, k
       keys.hi[j] = buf[(kPK + j) * 32 + lane];
     }
     float d[4];
-    keys.scores(qf, d);
+    keys.template scores<2>(qf, d);
     // column 0 lies in the lanes with mc == 0: d[0] for key mg, d[2] for key mg + 8
     float s0 = mg < n ? d[0] * scale : -INFINITY, s1 = mg + 8 < n ? d[2] * scale : -INFINITY;
     float mx = mc == 0 ? fmaxf(s0, s1) : -INFINITY;

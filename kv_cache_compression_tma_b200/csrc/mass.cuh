@@ -13,6 +13,14 @@ __device__ __forceinline__ float mass_row_lse(float lse_loc, float lse_hist) {
   return hi + log1pf(expf(-fabsf(lse_loc - lse_hist)));
 }
 
+// The same in 64 bits.  L is one number for all keys of a query, so with few queries its rounding does not
+// average out of the weights: at L = 20 half a unit of fp32 is already 1e-6 of every weight.
+__device__ __forceinline__ double mass_row_lse64(float lse_loc, float lse_hist) {
+  const double hi = fmaxf(lse_loc, lse_hist);
+  if (hi == -INFINITY) return INFINITY;
+  return hi + log1p(exp(-fabs(static_cast<double>(lse_loc) - static_cast<double>(lse_hist))));
+}
+
 // A key's bias is common to all its terms, so it multiplies the sum.  The terms stay finite for the
 // biases the attention admits: L covers the key itself, so s - L <= -b <= 64.  An excluded key
 // (bias -inf) is in no row's L, and its sum may be anything: it gets 0 whatever the sum is.

@@ -62,16 +62,19 @@ __global__ void __launch_bounds__(kThreads, 2) mass_few_kernel(const MassLaunch 
     __syncthreads();
   }
   // this lane's two query columns of each group; a column without a query, or a row without keys, adds 0
-  constexpr float kLog2e = 1.4426950408889634f;
-  const float sl2 = a.scale * kLog2e;
-  float nl[kCols][2];
+  constexpr double kLog2e = 1.4426950408889634;
+  const double sl2_64 = static_cast<double>(a.scale) * kLog2e;
+  const float sl2 = static_cast<float>(sl2_64), sl2_lo = static_cast<float>(sl2_64 - sl2);
+  float nl[kCols][2], nl_lo[kCols][2];  // -L log2(e) and what its rounding left
 #pragma unroll
   for (int col = 0; col < kCols; ++col)
 #pragma unroll
     for (int x = 0; x < 2; ++x) {
       const int i = col * 8 + 2 * c + x;
       const int64_t o = static_cast<int64_t>(head) * a.n_q + i;
-      nl[col][x] = i < a.n_q ? -kLog2e * mass_row_lse(a.lse_loc[o], a.lse_hist ? a.lse_hist[o] : -INFINITY) : -INFINITY;
+      const double l = i < a.n_q ? -kLog2e * mass_row_lse64(a.lse_loc[o], a.lse_hist ? a.lse_hist[o] : -INFINITY) : -INFINITY;
+      nl[col][x] = static_cast<float>(l);
+      nl_lo[col][x] = l > -INFINITY ? static_cast<float>(l - nl[col][x]) : 0.f;
     }
   for (; u < units; u += stride) {
     if (u + stride < units) load(u + stride, next);
@@ -83,12 +86,12 @@ __global__ void __launch_bounds__(kThreads, 2) mass_few_kernel(const MassLaunch 
         for (int j = 0; j < M::kPieces; ++j) q[j] = sq[col * M::kPieces + j][lane];
       }
       float d[4];
-      cur.scores(q, d);
+      cur.template scores<4>(q, d);
 #pragma unroll
       for (int x = 0; x < 2; ++x) {
         const bool live = nl[col][x] > -INFINITY || nl[col][x] != nl[col][x];  // a NaN stays one
-        lo += live ? fast_exp2(fmaf(d[x], sl2, nl[col][x])) : 0.f;
-        hi += live ? fast_exp2(fmaf(d[2 + x], sl2, nl[col][x])) : 0.f;
+        lo += live ? fast_exp2(fmaf(d[x], sl2, nl[col][x]) + fmaf(d[x], sl2_lo, nl_lo[col][x])) : 0.f;
+        hi += live ? fast_exp2(fmaf(d[2 + x], sl2, nl[col][x]) + fmaf(d[2 + x], sl2_lo, nl_lo[col][x])) : 0.f;
       }
     }
     lo = row_sum<4>(lo);
@@ -129,7 +132,7 @@ __global__ void __launch_bounds__(kThreads) mass_rows_kernel(const MassLaunch a)
   constexpr int kWarpKeys = R::kPerWarp * kRows;
   constexpr int kKeys = kSplit ? kWarpKeys : kWarps * kWarpKeys;  // keys per step of a CTA
   __shared__ float sq[kQTile][HD];
-  __shared__ float sl[kQTile];
+  __shared__ float sl[kQTile], sl_lo[kQTile];  // L and what its rounding left
   __shared__ float part[kSplit ? kWarps : 1][kWarpKeys];
   const int head = static_cast<int>(blockIdx.x % a.n_heads);  // heads first: CTAs that run together share rows
   const int64_t chunk = blockIdx.x / a.n_heads;
@@ -165,7 +168,9 @@ __global__ void __launch_bounds__(kThreads) mass_rows_kernel(const MassLaunch a)
           sq[x / HD][x % HD] = static_cast<float>(Q[(i0 + x / HD) * a.ld_q + x % HD]) * a.scale;
         if (threadIdx.x < nq) {
           const int64_t o = static_cast<int64_t>(head) * a.n_q + i0 + threadIdx.x;
-          sl[threadIdx.x] = mass_row_lse(a.lse_loc[o], a.lse_hist ? a.lse_hist[o] : -INFINITY);
+          const double l = mass_row_lse64(a.lse_loc[o], a.lse_hist ? a.lse_hist[o] : -INFINITY);
+          sl[threadIdx.x] = static_cast<float>(l);
+          sl_lo[threadIdx.x] = l < INFINITY ? static_cast<float>(l - sl[threadIdx.x]) : 0.f;
         }
         __syncthreads();
       }
@@ -176,7 +181,7 @@ __global__ void __launch_bounds__(kThreads) mass_rows_kernel(const MassLaunch a)
           const float4 w = *reinterpret_cast<const float4*>(&sq[i][lane * R::kVec + e]);
           qv[e] = w.x, qv[e + 1] = w.y, qv[e + 2] = w.z, qv[e + 3] = w.w;
         }
-        const float li = sl[i];
+        const float li = sl[i], li_lo = sl_lo[i];
 #pragma unroll
         for (int r = 0; r < kRows; ++r) {
           float kv[R::kVec], s = 0.f;
@@ -184,7 +189,7 @@ __global__ void __launch_bounds__(kThreads) mass_rows_kernel(const MassLaunch a)
 #pragma unroll
           for (int e = 0; e < R::kVec; ++e) s = fmaf(qv[e], kv[e], s);
           s = row_sum<R::kLanes>(s);
-          sum[r] += expf(s - li);
+          sum[r] += expf((s - li) - li_lo);
         }
       }
     }
