@@ -31,10 +31,13 @@ class LayerWork:
 
 
 def layer_forward(q, k_sink, v_sink, k_loc, v_loc, k_hist, v_hist, W, *, llayer: bool, w_transposed: bool = False,
-                  work: Optional[LayerWork] = None, out=None, stream=None):
+                  work: Optional[LayerWork] = None, out=None, stream=None, blocks=None, block: int = 128,
+                  q_block: int = 128):
     """One layer's attention and output projection after T_warm.
 
-    F-Layer (llayer False): attention over sink + local + history, y = A_full W.
+    F-Layer (llayer False): attention over sink + local + history, y = A_full W.  With `blocks` (int32 [H,
+    ceil(n_q / q_block), n_sel] from BlockIndex.select with the same block and q_block) the history is
+    read only in the blocks picked for each group of q_block queries.
     L-Layer (llayer True): attention over sink + local only (k_hist / v_hist are ignored and may be
     None), y = A_loc W, where the caller passes W_new as W.
     q and the k/v segments are [tokens, H, hd]; W is [d, d_out] (or [d_out, d] with w_transposed).
@@ -47,7 +50,12 @@ def layer_forward(q, k_sink, v_sink, k_loc, v_loc, k_hist, v_hist, W, *, llayer:
     if llayer:
         k_hist = k_loc[:0]
         v_hist = v_loc[:0]
-    ispa.dual_stream_attn(q, k_sink, v_sink, k_loc, v_loc, k_hist, v_hist, want_delta=False, stream=stream, **buf)
+    if blocks is not None and not llayer:
+        # the row-shaped lse buffers of a smaller chunk are not contiguous views: let the call allocate them
+        ispa.block_sparse_attn(q, k_sink, v_sink, k_loc, v_loc, k_hist, v_hist, blocks, block=block, q_block=q_block,
+                               o_loc=buf["o_loc"], o_full=buf["o_full"], want_delta=False, stream=stream)
+    else:
+        ispa.dual_stream_attn(q, k_sink, v_sink, k_loc, v_loc, k_hist, v_hist, want_delta=False, stream=stream, **buf)
     a = buf["o_loc"] if llayer else buf["o_full"]
     return ispa.project(a, W, w_transposed=w_transposed, out=out, stream=stream)
 

@@ -415,6 +415,27 @@ def test_streaming_loop_with_eviction_and_block_selection(cuda_ok):
     check_sparse(t, idx, 64, 1, ROW_TOL)
 
 
+@pytest.mark.parametrize("n_q,q_block", [(1, 1), (260, 128)])
+def test_layer_forward_over_selected_blocks(cuda_ok, n_q, q_block):
+    """llayer.layer_forward of an F-Layer with blocks: attention over the picks, then the projection; an
+    L-Layer ignores them."""
+    import torch
+    from kv_cache_compression_tma_b200 import ispa, llayer
+    H, hd = 2, 128
+    t, _ = sparse_case("bf16", H, hd, n_q, q_block, 30, 140, 900, 64, 4, 74)
+    bi = ispa.BlockIndex(H, hd, 1000, block=64)
+    bi.extend(t["k_hist"])
+    idx = bi.select(t["q"], 4, q_block=q_block)
+    W = tensor((H * hd, 1, H * hd), 75, torch.bfloat16, 1 / 16.0).flatten(1)
+    work = llayer.LayerWork(n_q + 40, H, hd, torch.bfloat16)
+    y = llayer.layer_forward(*t.values(), W, llayer=False, work=work, blocks=idx, block=64, q_block=q_block)
+    ref = orc.block_sparse(*(host(x) for x in t.values()), idx.cpu().numpy(), 64, q_block)
+    # the attention output's rounding (2^-8) and error (1e-2 in norm at most) pass through W, Y rounds once more
+    assert rel(host(y), ref["O_full"].reshape(n_q, -1) @ host(W)) <= 1.5e-2
+    local = llayer.layer_forward(*t.values(), W, llayer=True, work=work, blocks=idx, block=64, q_block=q_block)
+    assert rel(host(local), ref["O_loc"].reshape(n_q, -1) @ host(W)) <= 1.5e-2
+
+
 def test_captured_and_on_another_stream(cuda_ok):
     """All five calls captured once and replayed on new values in the same buffers, and run eagerly on a
     side stream: the same bits as eager calls on the current stream."""
