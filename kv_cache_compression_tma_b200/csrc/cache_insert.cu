@@ -449,7 +449,7 @@ cudaError_t launch_cache_insert(const InsertLaunch& a, cudaStream_t s, int* n_la
   const int64_t cand = static_cast<int64_t>(a.n) + a.n_new;
   int C = 1;
   while (C < kMaxCluster && cand > 16384ll * C && static_cast<int64_t>(a.n_heads) * 2 * C <= 128) C *= 2;
-  while (C < kMaxCluster && (a.n_new + C - 1) / C > kMaxNewSlice) C *= 2;
+  while (C < kMaxCluster && (cand > static_cast<int64_t>(kMaxCached) * C || (a.n_new + C - 1) / C > kMaxNewSlice)) C *= 2;
   const int old_per = (a.n + C - 1) / C, new_per = (a.n_new + C - 1) / C;
   const int cached = old_per + new_per <= kMaxCached;
   const size_t smem = 4ull * ((cached ? old_per + new_per : 0) + 2ll * new_per);

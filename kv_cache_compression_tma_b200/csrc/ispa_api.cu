@@ -52,6 +52,10 @@ bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) %
 // 40 heads 89 against 65 (each row reads its keys for itself).
 constexpr int64_t kBlockRowsMax = 96;
 
+// Heads of the bounded-history calls: one grid dimension of 65535 covers a row's 256-byte pieces at any
+// head_dim and type.
+constexpr int32_t kMaxHeads = 32767;
+
 // head dimensions of the kernels that spread a head's row over lanes
 bool rows_head_dim(int32_t hd) { return hd == 16 || hd == 32 || hd == 64 || hd == 128; }
 
@@ -421,7 +425,7 @@ ispa_status ispa_attn_mass(int32_t dtype, int32_t n_heads, int32_t head_dim, con
   if (dtype != ISPA_BF16 && dtype != ISPA_F32) return ISPA_ERR_INVALID_ARG;
   if (flags & ~static_cast<uint32_t>(ISPA_ATTN_CUDA_CORES)) return ISPA_ERR_INVALID_ARG;
   const int64_t lim = (1ll << 30);
-  if (n_heads < 1 || n_heads > 65535 || n_q < 0 || n_q > lim || n_k < 0 || n_k > lim) return ISPA_ERR_INVALID_ARG;
+  if (n_heads < 1 || n_heads > kMaxHeads || n_q < 0 || n_q > lim || n_k < 0 || n_k > lim) return ISPA_ERR_INVALID_ARG;
   if (!rows_head_dim(head_dim)) return ISPA_ERR_UNSUPPORTED;
   const bool cuda_cores = dtype == ISPA_F32 || (flags & ISPA_ATTN_CUDA_CORES) != 0;
   if (!cuda_cores && head_dim < 64) return ISPA_ERR_UNSUPPORTED;
@@ -453,7 +457,7 @@ ispa_status ispa_cache_insert(int32_t dtype, int32_t n_heads, int32_t head_dim, 
                               const float* mass_new, int64_t ld_mass_new, int32_t pos_new, int32_t keep_below,
                               int32_t keep_from, float* mass_out, int32_t* pos_out, int64_t ld_out, void* stream) {
   if (dtype != ISPA_BF16 && dtype != ISPA_F32) return ISPA_ERR_INVALID_ARG;
-  if (n_heads < 1 || n_heads > 65535 || n < 0 || n_new < 0 || capacity < n || capacity >= (1ll << 30))
+  if (n_heads < 1 || n_heads > kMaxHeads || n < 0 || n_new < 0 || capacity < n || capacity >= (1ll << 30))
     return ISPA_ERR_INVALID_ARG;
   if (!rows_head_dim(head_dim)) return ISPA_ERR_UNSUPPORTED;
   if (pos_new < 0 || pos_new > INT32_MAX - n_new) return ISPA_ERR_INVALID_ARG;
@@ -485,7 +489,7 @@ ispa_status ispa_cache_insert(int32_t dtype, int32_t n_heads, int32_t head_dim, 
 ispa_status ispa_block_means(int32_t dtype, int32_t n_heads, int32_t head_dim, const void* k, int64_t n_k, int64_t ld_k,
                              int32_t block, int64_t first_block, float* means, int64_t ld_means, void* stream) {
   if (dtype != ISPA_BF16 && dtype != ISPA_F32) return ISPA_ERR_INVALID_ARG;
-  if (n_heads < 1 || n_heads > 65535 || n_k < 0 || n_k > (1ll << 30) || block < 1 || first_block < 0) return ISPA_ERR_INVALID_ARG;
+  if (n_heads < 1 || n_heads > kMaxHeads || n_k < 0 || n_k > (1ll << 30) || block < 1 || first_block < 0) return ISPA_ERR_INVALID_ARG;
   if (!rows_head_dim(head_dim)) return ISPA_ERR_UNSUPPORTED;
   const int64_t d = static_cast<int64_t>(n_heads) * head_dim;
   if (first_block >= (n_k + block - 1) / block) return ISPA_OK;
@@ -503,7 +507,7 @@ ispa_status ispa_block_select(int32_t dtype, int32_t n_heads, int32_t head_dim, 
                               int32_t q_block, const float* means, int64_t n_blocks, int64_t ld_means, int32_t n_sel,
                               int32_t* idx_out, void* stream) {
   if (dtype != ISPA_BF16 && dtype != ISPA_F32) return ISPA_ERR_INVALID_ARG;
-  if (n_heads < 1 || n_heads > 65535 || n_q < 0 || n_q > (1ll << 30) || q_block < 1 || n_blocks < 0 || n_sel < 1)
+  if (n_heads < 1 || n_heads > kMaxHeads || n_q < 0 || n_q > (1ll << 30) || q_block < 1 || n_blocks < 0 || n_sel < 1)
     return ISPA_ERR_INVALID_ARG;
   if (!rows_head_dim(head_dim) || !block_select_supported(n_blocks)) return ISPA_ERR_UNSUPPORTED;
   if (n_q == 0) return ISPA_OK;
@@ -525,8 +529,8 @@ ispa_status ispa_block_sparse_attn(const ispa_attn_args* a, const int32_t* idx, 
   bool biased;
   const ispa_status checked = fill_attn(a, L, biased);
   if (checked != ISPA_OK) return checked;
-  if (n_sel < 0 || block < 1 || block > 65536 || q_block < 1 || a->n_heads > 65535) return ISPA_ERR_INVALID_ARG;
-  if (n_sel > 0 && (!idx || !aligned(idx, 4))) return ISPA_ERR_INVALID_ARG;
+  if (n_sel < 0 || block < 1 || block > 65536 || q_block < 1 || a->n_heads > kMaxHeads) return ISPA_ERR_INVALID_ARG;
+  if (n_sel > 0 && a->n_q > 0 && (!idx || !aligned(idx, 4))) return ISPA_ERR_INVALID_ARG;
   if (static_cast<int64_t>(n_sel) * block > (1ll << 30) || a->n_kv[0] > (1ll << 30) || a->n_kv[1] > (1ll << 30) ||
       a->n_kv[2] > (1ll << 30))
     return ISPA_ERR_INVALID_ARG;

@@ -531,7 +531,9 @@ class MassCache:
 
     def insert(self, k_new, v_new, mass_new=None, *, first: int = 0, recent: int = 0, stream=None):
         """Insert a frame's tokens; the first `first` positions of the stream and its newest `recent`
-        tokens are protected."""
+        tokens are protected (together at most `capacity`)."""
+        if first < 0 or recent < 0 or first + recent > self.capacity:
+            raise ValueError(f"first + recent must lie in 0 .. {self.capacity}")
         n_new = k_new.shape[0]
         keep_from = max(0, self.seen + n_new - recent) if recent > 0 else INT32_MAX
         self.n = cache_insert(self.k, self.v, self.mass, self.pos, self.n, k_new, v_new, mass_new, self.seen,
@@ -581,11 +583,18 @@ class BlockIndex:
         self.means = torch.zeros((-(-max_tokens // block), n_heads, head_dim), dtype=torch.float32, device=device)
 
     def extend(self, k, stream=None):
-        """Pool the blocks of the history k [n, H, hd] that its tokens since the last call touch."""
+        """Pool the blocks of the history k [n, H, hd] that its tokens since the last call touch.  The history
+        only grows at its end; reset() starts another."""
+        if k.shape[0] < self.n:
+            raise ValueError(f"the history had {self.n} tokens and now has {k.shape[0]}: reset() first")
         block_means(k, self.means, self.block, first=self.n // self.block, stream=stream)
         self.n = k.shape[0]
 
+    def reset(self):
+        self.n = 0
+
     def select(self, q, n_sel: int, *, q_block: int = 1, out=None, stream=None):
+        """The picks for each group of q_block queries; see block_select."""
         return block_select(q, self.means[:-(-self.n // self.block)], n_sel, q_block=q_block, out=out, stream=stream)
 
 

@@ -381,14 +381,14 @@ def tempcache_merge(k_cache, v_cache, count, k_new, v_new, idx, sim, threshold: 
 def attn_mass(q, k, lse_loc, lse_hist, mass, decay: float = 1.0, bias=None, scale: Optional[float] = None):
     """decay * mass + the softmax weight each key collects: q [n_q, H, hd], k [n_k, H, hd], lse_* [H, n_q]
     (lse_hist None: no history branch), mass [H, n_k], bias [H, n_k] or None.  The weight of key j in row
-    i is exp(scale q_i.k_j + bias_j) / (exp(lse_loc_i) + exp(lse_hist_i)); an excluded key (bias -inf)
-    and a row without keys (both -inf) give 0."""
+    i is exp(scale q_i.k_j + bias_j) / (exp(lse_loc_i) + exp(lse_hist_i)); an excluded key (bias -inf, or
+    with a factor exp(bias) of 0) and a row without keys (both -inf) give 0."""
     q, k = np.asarray(q, np.float64), np.asarray(k, np.float64)
     n_q, H, hd = q.shape
     scale = 1.0 / math.sqrt(hd) if scale is None else scale
     out = np.zeros((H, k.shape[0])) if decay == 0.0 else decay * np.asarray(mass, np.float64)
     for h in range(H):
-        live = np.ones(k.shape[0], bool) if bias is None else ~np.isneginf(bias[h])
+        live = np.ones(k.shape[0], bool) if bias is None else np.exp(np.asarray(bias[h], np.float64)) > 0
         b = 0.0 if bias is None else np.asarray(bias[h], np.float64)[live]
         for i in range(n_q):
             L = float(lse_loc[h, i]) if lse_hist is None else np.logaddexp(float(lse_loc[h, i]), float(lse_hist[h, i]))

@@ -125,13 +125,14 @@ def test_mass_rows_without_keys_masked_nan_and_decay_zero(cuda_ok, n_q):
     q, k = tensor((n_q, H, hd), 3, torch.bfloat16, 2.0, pad=8), tensor((n_k, H, hd), 4, torch.bfloat16, pad=16)
     bias = torch.zeros((H, n_k + 1), device="cuda")[:, 1:]  # 4-byte aligned only
     bias[:, 7] = -float("inf")
+    bias[:, 9] = torch.finfo(torch.float32).min  # as good as excluded
     ll = lse_of(q, k, host(bias))
     k[7] = float("nan")
+    k[9] = 1000.0
     ll[:, n_q // 2] = -float("inf")
     mass = torch.full((H, n_k), float("nan"), device="cuda")
     check_mass(q, k, ll, None, mass, 0.0, bias)
-    assert (mass[:, 7] == 0).all()
-    k[7] = 0
+    assert (mass[:, [7, 9]] == 0).all()
     for lead in (0, 1):
         qq, kk = tensor((n_q, H, 32), 5, torch.bfloat16, 2.0, 1, lead), tensor((n_k, H, 32), 6, torch.bfloat16, 1.0, 1, lead)
         check_mass(qq, kk, lse_of(qq, kk), None, mass.fill_(1.0), 1.0, cuda_cores=True)
@@ -377,6 +378,71 @@ def test_sparse_odd_lists(cuda_ok):
     assert e.value.status == ispa.ISPA_ERR_UNSUPPORTED
 
 
+@pytest.mark.parametrize("dtype,n_q,q_block,n_hist,n_sel", [("bf16", 3, 1, 0, 2), ("bf16", 200, 128, 0, 2), ("fp32", 3, 2, 0, 2),
+                                                            ("bf16", 0, 1, 10, 2), ("bf16", 0, 128, 10, 2)])
+def test_sparse_empty_history_and_no_queries(cuda_ok, dtype, n_q, q_block, n_hist, n_sel):
+    """An empty history with a list that names blocks anyway, and a call without queries."""
+    import torch
+    t, idx = sparse_case(dtype, 2, 64, n_q, q_block, 5, 70, n_hist, 64, n_sel, 66)
+    idx.fill_(0)
+    out = check_sparse(t, idx, 64, q_block, F32_TOL if dtype == "fp32" else ATTN_TOL) if n_q else None
+    if out is not None:
+        assert torch.isneginf(out["lse_hist"]).all()
+    else:
+        from kv_cache_compression_tma_b200 import ispa
+        assert ispa.block_sparse_attn(*t.values(), idx, block=64, q_block=q_block)["o_loc"].shape == (0, 128)
+
+
+@pytest.mark.parametrize("n_q,q_block", [(1, 1), (150, 128)])
+def test_sparse_outputs_stay_inside_their_rows(cuda_ok, n_q, q_block):
+    """Outputs that are views of wider, longer buffers: nothing outside them is written."""
+    import torch
+    from kv_cache_compression_tma_b200 import ispa
+    t, idx = sparse_case("bf16", 2, 128, n_q, q_block, 5, 70, 300, 64, 3, 67)
+    wide = {w: torch.full((n_q + 9, 256 + 16), 7.0, dtype=torch.bfloat16, device="cuda") for w in ("o_loc", "o_full", "d_out")}
+    views = {w: x[4:4 + n_q, :256] for w, x in wide.items()}
+    check_sparse(t, idx, 64, q_block, ATTN_TOL, **views)
+    for x in wide.values():
+        assert (x[:4] == 7).all() and (x[4 + n_q:] == 7).all() and (x[:, 256:] == 7).all()
+    with pytest.raises(ValueError):
+        ispa.block_sparse_attn(*t.values(), idx, block=64, q_block=q_block, o_loc=views["o_loc"][:, :255])
+
+
+# ------------------------------------------------------------------------------------------ far offsets
+def test_offsets_past_32_bits(cuda_ok):
+    """Token strides of 2^30 elements: the last of five tokens starts past 2^32 elements, 8 GB in."""
+    import torch
+    from kv_cache_compression_tma_b200 import ispa
+    n, H, hd, ld = 5, 1, 64, 2 ** 30
+    if torch.cuda.mem_get_info()[0] < 25e9:
+        pytest.skip("needs 25 GB of free device memory")
+    far = [torch.empty((n - 1) * ld + H * hd, dtype=torch.bfloat16, device="cuda").as_strided((n, H, hd), (ld, hd, 1)) for _ in range(2)]
+    near = [tensor((n, H, hd), 68 + i, torch.bfloat16) for i in range(2)]
+    for f, x in zip(far, near):
+        f.copy_(x)
+    for n_q in (3, 40):
+        q = tensor((n_q, H, hd), 69, torch.bfloat16, 2.0)
+        ll = lse_of(q, near[0])
+        got, want = (ispa.attn_mass(q, k, ll, None, torch.zeros((H, n), device="cuda")) for k in (far[0], near[0]))
+        assert torch.equal(got, want)
+    idx = torch.tensor([[[0, 2]]], dtype=torch.int32, device="cuda")
+    for dtype_q, q_block in ((3, 3), (130, 256)):
+        q = tensor((dtype_q, H, hd), 69, torch.bfloat16, 2.0)
+        a, b = (ispa.block_sparse_attn(q, *kv, *kv, *kv, idx, block=64 if q_block > 128 else 2, q_block=q_block,
+                                       cuda_cores=q_block == 3) for kv in (far, near))
+        assert all(torch.equal(a[w], b[w]) for w in a)
+    means = [torch.zeros((3, H, hd), device="cuda") for _ in range(2)]
+    ispa.block_means(far[0], means[0], 2)
+    ispa.block_means(near[0], means[1], 2)
+    assert torch.equal(*means)
+    new = [tensor((2, H, hd), 70 + i, torch.bfloat16) for i in range(2)]
+    state = [(torch.arange(n, device="cuda", dtype=torch.float32).flip(0)[None].contiguous(), torch.arange(n, dtype=torch.int32, device="cuda")[None].contiguous()) for _ in range(2)]
+    for kv, (m, p) in zip((far, near), state):
+        ispa.cache_insert(*kv, m, p, n, *new, torch.full((1, 2), 9.0, device="cuda"), n)
+    assert torch.equal(far[0], near[0]) and torch.equal(far[1], near[1]) and torch.equal(state[0][0], state[1][0])
+    assert torch.equal(near[0][4], new[0][1]) and torch.equal(near[0][3], new[0][0])
+
+
 # ------------------------------------------------------------------------------------------ together
 def test_streaming_loop_with_eviction_and_block_selection(cuda_ok):
     """Chunks stream through a MassCache of fixed size: attend, accumulate, insert; then a BlockIndex over
@@ -434,6 +500,66 @@ def test_layer_forward_over_selected_blocks(cuda_ok, n_q, q_block):
     assert rel(host(y), ref["O_full"].reshape(n_q, -1) @ host(W)) <= 1.5e-2
     local = llayer.layer_forward(*t.values(), W, llayer=True, work=work, blocks=idx, block=64, q_block=q_block)
     assert rel(host(local), ref["O_loc"].reshape(n_q, -1) @ host(W)) <= 1.5e-2
+
+
+def test_two_streams_at_once(cuda_ok):
+    """The same calls on two streams, interleaved, on separate buffers: no state is shared."""
+    import torch
+    from kv_cache_compression_tma_b200 import ispa
+    H, hd, n, n_q = 4, 128, 3000, 300
+    sets = []
+    for s in range(2):
+        q, k, v = (tensor((m, H, hd), 95 + 3 * s + i, torch.bfloat16, sc) for i, (m, sc) in enumerate(((n_q, 2.0), (n, 1.0), (n, 1.0))))
+        sets.append(dict(q=q, k=k, v=v, ll=torch.full((H, n_q), 8.0 + s, device="cuda"), means=torch.zeros((24, H, hd), device="cuda")))
+
+    def step(x):
+        ispa.block_means(x["k"], x["means"], 128)
+        idx = ispa.block_select(x["q"], x["means"], 5, q_block=128)
+        o = ispa.block_sparse_attn(x["q"], x["k"], x["v"], x["k"], x["v"], x["k"], x["v"], idx, block=128, q_block=128)
+        m = ispa.attn_mass(x["q"], x["k"], x["ll"], None, torch.zeros((H, n), device="cuda"))
+        k, v, pos = x["k"].clone(), x["v"].clone(), torch.arange(n, dtype=torch.int32, device="cuda").repeat(H, 1)
+        ispa.cache_insert(k, v, m, pos, n, x["q"], x["q"], None, n, keep_from=n + 100)
+        return [idx, m, k, pos, *o.values()]
+
+    want = [step(x) for x in sets]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    got = [None, None]
+    for _ in range(3):
+        for i, st in enumerate(streams):
+            with torch.cuda.stream(st):
+                got[i] = step(sets[i])
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for w, g in zip(want, got) for a, b in zip(w, g))
+    assert ispa.get_device_status() == ispa.ISPA_OK
+
+
+def test_host_checks_of_the_binding(cuda_ok):
+    """Host tensors, wrong shapes and types, heads that are not dense: refused before a launch."""
+    import torch
+    from kv_cache_compression_tma_b200 import ispa
+    k, f = tensor((8, 2, 64), 1, torch.bfloat16), torch.zeros((2, 8), device="cuda")
+    i = torch.zeros((2, 8), dtype=torch.int32, device="cuda")
+    n0 = ispa.launch_count()
+    bad = [lambda: ispa.attn_mass(k, k.cpu(), f, None, f), lambda: ispa.attn_mass(k, k, f, None, f[:, :7]),
+           lambda: ispa.attn_mass(k, k.transpose(1, 2).contiguous().transpose(1, 2), f, None, f),
+           lambda: ispa.attn_mass(k, k, f.double(), None, f), lambda: ispa.attn_mass(k, k[:, :1], f, None, f),
+           lambda: ispa.cache_insert(k, k[:7], f, i, 8, k, k, None, 8), lambda: ispa.cache_insert(k, k, f, i[:, :7], 8, k, k, None, 8),
+           lambda: ispa.cache_insert(k, k, f, i, 8, k.float(), k, None, 8), lambda: ispa.cache_insert(k, k, f[:, :4], i[:, :4], 4, k, k, None, 8),
+           lambda: ispa.block_means(k, torch.zeros((1, 2, 64), device="cuda"), 4), lambda: ispa.block_select(k, k.float(), 2, out=i[:, :1]),
+           lambda: ispa.block_sparse_attn(k, k, k[:7], k, k, k, k, i[:, :8, None].contiguous(), block=4),
+           lambda: ispa.block_sparse_attn(k, k, k, k, k, k, k, i[:, :8, None].contiguous().long(), block=4),
+           lambda: ispa.MassCache(2, 64, 8).insert(k, k, first=4, recent=5)]
+    for call in bad:
+        with pytest.raises(ValueError):
+            call()
+    bi = ispa.BlockIndex(2, 64, 64, block=4)
+    bi.extend(k)
+    with pytest.raises(ValueError):
+        bi.extend(k[:5])
+    bi.reset()
+    bi.extend(k[:5])
+    assert bi.select(k, 3).shape == (2, 8, 3) and ispa.launch_count() == n0 + 3
 
 
 def test_captured_and_on_another_stream(cuda_ok):
