@@ -15,14 +15,14 @@
 // it computes.  Sixteen warps, because the work per element is a chain (scale, exponential, add) whose
 // latency eight do not cover.
 //
-// Bound: the exponentials and the products together, under the power cap.  12 heads x 4680 queries x
-// 14040 keys: 0.204 ms (202 GFLOP, 0.124 ms at the measured bf16 peak; 0.171 ms if the special-function
-// unit did every exponential at 1965 MHz), with 71 % of that unit, 48 % of the multiply-add pipes and
-// 47 % of the tensor pipe busy at a clock of 1.6 to 1.8 GHz.  Measured beside it, 12 heads: 0.246 ms with
-// 8 warps and 0.234 with 16 while a lone lane issued the MMAs (their operands then move to uniform
-// registers one by one; umma_ts_warp), 0.226 without the polynomial exponential, 0.205 with products
-// 192 or 256 queries wide on two accumulators, 0.235 with 96 on four (each completion costs the tensor
-// pipe some 400 clocks).
+// Bound: exponentials and products together, under the power cap.  12 heads x 4680 queries x 14040 keys:
+// 0.204 ms in a short burst (202 GFLOP, 0.124 ms at the measured bf16 peak; 0.171 ms if the
+// special-function unit did every exponential at 1965 MHz), 0.237 ms back to back at 995 W and 1.6 GHz,
+// with 71 % of that unit, 48 % of the multiply-add pipes and 47 % of the tensor pipe busy.  Measured
+// beside it: 0.246 ms with 8 warps and 0.234 with 16 while a lone lane issued the MMAs (the warp-uniform
+// form has fewer instructions to squeeze in between the sixteen busy warps; 0.243 -> 0.226 on one
+// variant), 0.226 without the polynomial exponential, 0.205 with products 192 or 256 queries wide on two
+// accumulators, 0.235 with 96 on four (more hand-offs).  A burst without any exponential runs at 0.16 ms.
 //
 // Warp roles (608 threads): warp 0 TMA producer, warp 1 TMEM and the MMAs, warp 2 idle, warps 3..18 the
 // four warpgroups.  TMEM columns: [0,384) three accumulators, [384,512) two key tiles (bf16 pairs).

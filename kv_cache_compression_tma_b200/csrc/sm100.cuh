@@ -159,7 +159,8 @@ __device__ __forceinline__ void umma_ts(uint32_t d_tmem, uint32_t a_tmem, uint64
 }
 
 // Forms for a whole converged warp, one lane of which (`leader`) issues: the operands then stay in uniform
-// registers, where a lone lane's code has to move each of them there before every instruction.
+// registers, where a lone lane's code moves them there before every instruction.  Alone on an SM both
+// forms reach the tensor pipe's rate; next to busy warps the shorter one waits less for issue slots.
 __device__ __forceinline__ uint32_t elect_leader() {
   uint32_t l;
   asm volatile(
