@@ -182,7 +182,8 @@ __global__ void __launch_bounds__(Kind<T, HD, kAligned>::kThreads, Kind<T, HD, k
 #pragma unroll
         for (int e = 0; e < 4; ++e) ab[t][e] *= alpha;
     }
-    const float p0 = fast_exp2(s0 - mx), p1 = fast_exp2(s1 - mx);
+    const float ref = mx == -INFINITY ? 0.f : mx;  // keys that score -inf weigh 0, the first ones too
+    const float p0 = fast_exp2(s0 - ref), p1 = fast_exp2(s1 - ref);
     lb += p0 + p1;  // of the lanes with mc == 0
     // weights as the second operand: column mg, keys 2 mc + {0, 1} and 8 more; column 0 the rounded
     // weights, column 1 what the rounding left, the others zero
@@ -232,8 +233,8 @@ __global__ void __launch_bounds__(Kind<T, HD, kAligned>::kThreads, Kind<T, HD, k
       s[i] = i * R::kPerWarp + grp < n ? d : -INFINITY;
       mx = fmaxf(mx, s[i]);
     }
-    if (grp >= n && mb == -INFINITY) return;  // this lane group has met no key yet (no shuffles below)
-    const float alpha = exp2f(mb - mx);
+    const float ref = mx == -INFINITY ? 0.f : mx;  // no key yet, or keys that score -inf: weight 0
+    const float alpha = exp2f(mb - ref);
     mb = mx;
     lb *= alpha;
 #pragma unroll
@@ -241,7 +242,7 @@ __global__ void __launch_bounds__(Kind<T, HD, kAligned>::kThreads, Kind<T, HD, k
 #pragma unroll
     for (int i = 0; i < kLoads; ++i) {
       float vv[R::kVec];
-      const float p = exp2f(s[i] - mx);
+      const float p = exp2f(s[i] - ref);
       unpack<T>(vw[i], vv);
       lb += p;
 #pragma unroll

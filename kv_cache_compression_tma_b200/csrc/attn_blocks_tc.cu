@@ -336,7 +336,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_blocks_tc_kernel(const __gri
         m = mx;
         rescale = true;
       }
-      const uint64_t sl2x2 = pack_f2(sl2, sl2), negm2 = pack_f2(-m, -m);
+      const float neg_m = m == -INFINITY ? 0.f : -m;  // a row whose keys so far all score -inf: weights 0
+      const uint64_t sl2x2 = pack_f2(sl2, sl2), negm2 = pack_f2(neg_m, neg_m);
       uint64_t acc[4] = {0ull, 0ull, 0ull, 0ull};
       uint32_t pk[kCols / 2];
 #pragma unroll
@@ -410,7 +411,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_blocks_tc_kernel(const __gri
         w_hist = bb / (a + bb);
       }
       const float inv_l_loc = 1.f / l_loc_row;
-      const float inv_l_hist = has_hist ? 1.f / l_hist_row : 0.f;
+      const float inv_l_hist = has_hist && l_hist_row != 0.f ? 1.f / l_hist_row : 0.f;
       const uint32_t oa_addr = tmem + lane_addr + 256 + part * kOCols;
       auto put = [&](int which, int col, const float* v8) {  // 8 values at tile column col, 128-byte swizzle
         uint4 w;

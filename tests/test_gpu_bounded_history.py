@@ -393,6 +393,30 @@ def test_sparse_empty_history_and_no_queries(cuda_ok, dtype, n_q, q_block, n_his
         assert ispa.block_sparse_attn(*t.values(), idx, block=64, q_block=q_block)["o_loc"].shape == (0, 128)
 
 
+@pytest.mark.parametrize("dtype,n_q,q_block,block", [("bf16", 2, 1, 64), ("fp32", 2, 1, 64), ("bf16", 130, 128, 64), ("bf16", 130, 128, 128)])
+def test_sparse_keys_that_score_minus_infinity(cuda_ok, dtype, n_q, q_block, block):
+    """Keys whose products overflow to -inf (the first ones of a branch, too) weigh nothing; a history of
+    nothing else gives lse_hist = -inf and O_full = O_loc."""
+    import torch
+    from kv_cache_compression_tma_b200 import ispa
+    t, _ = sparse_case(dtype, 1, 64, n_q, q_block, 140, 20, 3 * block, block, 1, 68)
+    t["q"].copy_(t["q"].abs() + 1)
+    t["k_sink"][:130] = -3e38
+    t["k_hist"][:2 * block] = -3e38
+    groups = -(-n_q // q_block)
+    idx = torch.tensor([[[0, 1, 2]] * (groups - 1) + [[0, 1, -1]]], dtype=torch.int32, device="cuda")
+    out = ispa.block_sparse_attn(*t.values(), idx, block=block, q_block=q_block)
+    clean = dict(t, k_sink=t["k_sink"][130:], v_sink=t["v_sink"][130:])
+    last = torch.tensor([[[2]] * (groups - 1) + [[-1]]], dtype=torch.int32, device="cuda")
+    want = ispa.block_sparse_attn(*clean.values(), last, block=block, q_block=q_block)
+    tol = F32_TOL if dtype == "fp32" else ATTN_TOL
+    for w in ("o_loc", "o_full", "d"):
+        assert rel(host(out[w]), host(want[w])) <= tol[w], w
+    for w in ("lse_loc", "lse_hist"):
+        a, b = host(out[w]), host(want[w])
+        assert np.array_equal(np.isneginf(a), np.isneginf(b)) and np.allclose(a[np.isfinite(b)], b[np.isfinite(b)], atol=tol[w])
+
+
 @pytest.mark.parametrize("n_q,q_block", [(1, 1), (150, 128)])
 def test_sparse_outputs_stay_inside_their_rows(cuda_ok, n_q, q_block):
     """Outputs that are views of wider, longer buffers: nothing outside them is written."""
