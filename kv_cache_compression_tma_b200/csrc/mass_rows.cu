@@ -162,8 +162,8 @@ __global__ void __launch_bounds__(kThreads) mass_rows_kernel(const MassLaunch a)
     float sum[kRows] = {};
     for (int64_t i0 = 0; i0 < a.n_q; i0 += kQTile) {
       const int nq = static_cast<int>(a.n_q - i0 < kQTile ? a.n_q - i0 : kQTile);
-      if (step == 0 || a.n_q > kQTile) {  // a lone tile of queries stays staged over the steps
-        if (i0 > 0 || step > 0) __syncthreads();
+      if (step == 0) {  // several steps have a lone tile of queries, which stays staged
+        if (i0 > 0) __syncthreads();
         for (int x = threadIdx.x; x < nq * HD; x += kThreads)
           sq[x / HD][x % HD] = static_cast<float>(Q[(i0 + x / HD) * a.ld_q + x % HD]) * a.scale;
         if (threadIdx.x < nq) {
