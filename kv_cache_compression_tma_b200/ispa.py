@@ -626,7 +626,7 @@ def block_sparse_attn(q, k_sink, v_sink, k_loc, v_loc, k_hist, v_hist, idx, *, b
     for o in (o_loc, o_full, d_out):
         if o is None:
             continue
-        if o.shape != shape or o.dtype != dtype or (n_q > 1 and o.stride() != (ld_o, 1)):
+        if o.shape != shape or o.dtype != dtype or o.stride()[1] != 1 or (n_q > 1 and o.stride()[0] != ld_o):
             raise ValueError(f"outputs must be {dtype} {list(shape)} with one row stride")
         if o.get_device() != dev:
             _on_current_device(o)

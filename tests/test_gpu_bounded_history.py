@@ -430,6 +430,10 @@ def test_sparse_outputs_stay_inside_their_rows(cuda_ok, n_q, q_block):
         assert (x[:4] == 7).all() and (x[4 + n_q:] == 7).all() and (x[:, 256:] == 7).all()
     with pytest.raises(ValueError):
         ispa.block_sparse_attn(*t.values(), idx, block=64, q_block=q_block, o_loc=views["o_loc"][:, :255])
+    for w in views:  # columns apart, a lone row's too
+        with pytest.raises(ValueError):
+            apart = torch.zeros((n_q, 512), dtype=torch.bfloat16, device="cuda")[:, ::2]
+            ispa.block_sparse_attn(*t.values(), idx, block=64, q_block=q_block, **{w: apart})
 
 
 # ------------------------------------------------------------------------------------------ far offsets
