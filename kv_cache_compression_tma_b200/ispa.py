@@ -6,6 +6,7 @@ is no fallback.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import math
 import os
@@ -134,6 +135,13 @@ def _stream(stream=None) -> int:
     if stream is None:  # the raw handle: a Stream object costs several microseconds per call
         return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
     return int(stream.cuda_stream)
+
+
+def _alloc_on(stream):
+    """Where a call on `stream` allocates what it returns or drops: from that stream's memory, whose reuse
+    follows the call's kernels."""
+    import torch
+    return contextlib.nullcontext() if stream is None else torch.cuda.stream(stream)
 
 
 def _dtype_code(t) -> int:
@@ -566,7 +574,8 @@ def block_select(q, means, n_sel: int, *, q_block: int = 1, out=None, stream=Non
     n_blocks, ld_means = _heads_rows(means, "means", H, hd, torch.float32, dev)
     shape = (H, -(-n_q // q_block), n_sel)
     if out is None:
-        out = torch.empty(shape, dtype=torch.int32, device=q.device)
+        with _alloc_on(stream):
+            out = torch.empty(shape, dtype=torch.int32, device=q.device)
     _check(lib().ispa_block_select(_dtype_code(q), H, hd, q.data_ptr(), n_q, ld_q, q_block, means.data_ptr(), n_blocks,
                                    ld_means, n_sel, _dense(out, "out", shape, torch.int32, dev), _stream(stream)),
            "ispa_block_select")
@@ -615,14 +624,19 @@ def block_sparse_attn(q, k_sink, v_sink, k_loc, v_loc, k_hist, v_hist, idx, *, b
     nh, ld_kh = _heads_rows(k_hist, "k_hist", H, hd, dtype, dev)
     ld_vh = _heads_rows(v_hist, "v_hist", H, hd, dtype, dev, nh)[1]
     shape, ld_o = (n_q, H * hd), H * hd
-    if o_loc is None:
-        o_loc = torch.empty(shape, dtype=dtype, device=q.device)
-    elif n_q > 1:
+    if o_loc is not None and n_q > 1:
         ld_o = o_loc.stride()[0]
-    if o_full is None:
-        o_full = torch.empty_strided(shape, (ld_o, 1), dtype=dtype, device=q.device)
-    if d_out is None and want_delta:
-        d_out = torch.empty_strided(shape, (ld_o, 1), dtype=dtype, device=q.device)
+    with _alloc_on(stream):
+        if o_loc is None:
+            o_loc = torch.empty(shape, dtype=dtype, device=q.device)
+        if o_full is None:
+            o_full = torch.empty_strided(shape, (ld_o, 1), dtype=dtype, device=q.device)
+        if d_out is None and want_delta:
+            d_out = torch.empty_strided(shape, (ld_o, 1), dtype=dtype, device=q.device)
+        if lse_loc is None:
+            lse_loc = torch.empty((H, n_q), dtype=f32, device=q.device)
+        if lse_hist is None:
+            lse_hist = torch.empty((H, n_q), dtype=f32, device=q.device)
     for o in (o_loc, o_full, d_out):
         if o is None:
             continue
@@ -630,10 +644,6 @@ def block_sparse_attn(q, k_sink, v_sink, k_loc, v_loc, k_hist, v_hist, idx, *, b
             raise ValueError(f"outputs must be {dtype} {list(shape)} with one row stride")
         if o.get_device() != dev:
             _on_current_device(o)
-    if lse_loc is None:
-        lse_loc = torch.empty((H, n_q), dtype=f32, device=q.device)
-    if lse_hist is None:
-        lse_hist = torch.empty((H, n_q), dtype=f32, device=q.device)
     n_sel = idx.shape[-1]
     a = AttnArgs(_dtype_code(q), H, hd, ISPA_ATTN_CUDA_CORES if cuda_cores else 0, n_q, (ns, nl, nh), q.data_ptr(), ld_q,
                  (k_sink.data_ptr(), k_loc.data_ptr(), k_hist.data_ptr()),

@@ -590,6 +590,22 @@ def test_host_checks_of_the_binding(cuda_ok):
     assert bi.select(k, 3).shape == (2, 8, 3) and ispa.launch_count() == n0 + 3
 
 
+def test_results_of_a_call_on_a_stream_come_from_its_memory(cuda_ok):
+    """A call given a stream allocates from that stream's memory: nothing that another stream still uses is
+    written, and what the call drops is not handed out before its kernels are done."""
+    import torch
+    from kv_cache_compression_tma_b200 import ispa
+    t, idx = sparse_case("bf16", 2, 128, 3, 1, 5, 70, 300, 64, 3, 69)
+    means = ispa.block_means(t["k_hist"], torch.zeros((5, 2, 128), device="cuda"), 64)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    out = ispa.block_sparse_attn(*t.values(), idx, block=64, stream=side)
+    out["idx"] = ispa.block_select(t["q"], means, 3, stream=side)
+    side.synchronize()
+    owner = {b["address"]: s["stream"] for s in torch.cuda.memory_snapshot() for b in s["blocks"]}
+    assert all(owner[x.data_ptr()] == side.cuda_stream for x in out.values())
+
+
 def test_captured_and_on_another_stream(cuda_ok):
     """All five calls captured once and replayed on new values in the same buffers, and run eagerly on a
     side stream: the same bits as eager calls on the current stream."""
