@@ -198,14 +198,22 @@ def _heads_rows(t, what: str, H: int, hd: int, dtype, device: int, n: Optional[i
     return shape[0], stride[0] if shape[0] > 1 else H * hd
 
 
+def _pieces(n: int, size: int, what: str) -> int:
+    """How many pieces of `size` cover n."""
+    if size < 1:
+        raise ValueError(f"{what} must be at least 1")
+    return -(-n // size)
+
+
 def _state_rows(t, what: str, H: int, cols: int, dtype, device: int) -> int:
-    """Row stride of a per-head array [H, >= cols] of this type on the current device, columns contiguous."""
+    """Row stride of a per-head array [H, >= cols] of this type on the current device, columns contiguous; a
+    lone head's row has none, and the largest length stands for it in every array."""
     shape, stride = t.shape, t.stride()
     if len(shape) != 2 or shape[0] != H or shape[1] < cols or t.dtype != dtype or (stride[1] != 1 and shape[1] > 1):
         raise ValueError(f"{what}: expected {dtype} [{H}, >= {cols}] with contiguous columns")
     if t.get_device() != device:
         _on_current_device(t)
-    return stride[0] if H > 1 else max(shape[1], 1)
+    return stride[0] if H > 1 else 1 << 30
 
 
 def _dense(t, what: str, shape, dtype, device: int) -> int:
@@ -557,7 +565,7 @@ def block_means(k, means, block: int, *, first: int = 0, stream=None):
     _, H, hd = k.shape
     n_k, ld_k = _heads_rows(k, "k", H, hd, k.dtype, dev)
     rows, ld_means = _heads_rows(means, "means", H, hd, torch.float32, dev)
-    if rows < -(-n_k // block):
+    if rows < _pieces(n_k, block, "block"):
         raise ValueError("means has fewer rows than k has blocks")
     _check(lib().ispa_block_means(_dtype_code(k), H, hd, k.data_ptr(), n_k, ld_k, block, first, means.data_ptr(),
                                   ld_means, _stream(stream)), "ispa_block_means")
@@ -572,7 +580,7 @@ def block_select(q, means, n_sel: int, *, q_block: int = 1, out=None, stream=Non
     n_q, H, hd = q.shape
     _, ld_q = _heads_rows(q, "q", H, hd, q.dtype, dev)
     n_blocks, ld_means = _heads_rows(means, "means", H, hd, torch.float32, dev)
-    shape = (H, -(-n_q // q_block), n_sel)
+    shape = (H, _pieces(n_q, q_block, "q_block"), n_sel)
     if out is None:
         with _alloc_on(stream):
             out = torch.empty(shape, dtype=torch.int32, device=q.device)
@@ -589,7 +597,7 @@ class BlockIndex:
     def __init__(self, n_heads: int, head_dim: int, max_tokens: int, block: int = 128, device="cuda"):
         import torch
         self.block, self.n = block, 0
-        self.means = torch.zeros((-(-max_tokens // block), n_heads, head_dim), dtype=torch.float32, device=device)
+        self.means = torch.zeros((_pieces(max_tokens, block, "block"), n_heads, head_dim), dtype=torch.float32, device=device)
 
     def extend(self, k, stream=None):
         """Pool the blocks of the history k [n, H, hd] that its tokens since the last call touch.  The history
@@ -604,7 +612,7 @@ class BlockIndex:
 
     def select(self, q, n_sel: int, *, q_block: int = 1, out=None, stream=None):
         """The picks for each group of q_block queries; see block_select."""
-        return block_select(q, self.means[:-(-self.n // self.block)], n_sel, q_block=q_block, out=out, stream=stream)
+        return block_select(q, self.means[:_pieces(self.n, self.block, "block")], n_sel, q_block=q_block, out=out, stream=stream)
 
 
 def block_sparse_attn(q, k_sink, v_sink, k_loc, v_loc, k_hist, v_hist, idx, *, block: int, q_block: int = 1, o_loc=None,
@@ -644,13 +652,13 @@ def block_sparse_attn(q, k_sink, v_sink, k_loc, v_loc, k_hist, v_hist, idx, *, b
             raise ValueError(f"outputs must be {dtype} {list(shape)} with one row stride")
         if o.get_device() != dev:
             _on_current_device(o)
-    n_sel = idx.shape[-1]
+    n_sel, groups = idx.shape[-1], _pieces(n_q, q_block, "q_block")
     a = AttnArgs(_dtype_code(q), H, hd, ISPA_ATTN_CUDA_CORES if cuda_cores else 0, n_q, (ns, nl, nh), q.data_ptr(), ld_q,
                  (k_sink.data_ptr(), k_loc.data_ptr(), k_hist.data_ptr()),
                  (v_sink.data_ptr(), v_loc.data_ptr(), v_hist.data_ptr()), (ld_ks, ld_kl, ld_kh), (ld_vs, ld_vl, ld_vh),
                  softmax_scale, 0.0, o_loc.data_ptr(), o_full.data_ptr(), ld_o,
                  _dense(lse_loc, "lse_loc", (H, n_q), f32, dev), _dense(lse_hist, "lse_hist", (H, n_q), f32, dev), _ptr(d_out))
-    _check(lib().ispa_block_sparse_attn(ctypes.byref(a), _dense(idx, "idx", (H, -(-n_q // q_block), n_sel), torch.int32, dev),
+    _check(lib().ispa_block_sparse_attn(ctypes.byref(a), _dense(idx, "idx", (H, groups, n_sel), torch.int32, dev),
                                         n_sel, block, q_block, _stream(stream)), "ispa_block_sparse_attn")
     return {"o_loc": o_loc, "o_full": o_full, "d": d_out, "lse_loc": lse_loc, "lse_hist": lse_hist}
 

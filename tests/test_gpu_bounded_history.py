@@ -577,7 +577,9 @@ def test_host_checks_of_the_binding(cuda_ok):
            lambda: ispa.block_means(k, torch.zeros((1, 2, 64), device="cuda"), 4), lambda: ispa.block_select(k, k.float(), 2, out=i[:, :1]),
            lambda: ispa.block_sparse_attn(k, k, k[:7], k, k, k, k, i[:, :8, None].contiguous(), block=4),
            lambda: ispa.block_sparse_attn(k, k, k, k, k, k, k, i[:, :8, None].contiguous().long(), block=4),
-           lambda: ispa.MassCache(2, 64, 8).insert(k, k, first=4, recent=5)]
+           lambda: ispa.block_means(k, torch.zeros((8, 2, 64), device="cuda"), 0), lambda: ispa.block_select(k, k.float(), 2, q_block=0),
+           lambda: ispa.block_sparse_attn(k, k, k, k, k, k, k, i[:, :8, None].contiguous(), block=4, q_block=0),
+           lambda: ispa.BlockIndex(2, 64, 64, block=0), lambda: ispa.MassCache(2, 64, 8).insert(k, k, first=4, recent=5)]
     for call in bad:
         with pytest.raises(ValueError):
             call()
@@ -588,6 +590,24 @@ def test_host_checks_of_the_binding(cuda_ok):
     bi.reset()
     bi.extend(k[:5])
     assert bi.select(k, 3).shape == (2, 8, 3) and ispa.launch_count() == n0 + 3
+
+
+def test_a_lone_head_has_no_row_stride(cuda_ok):
+    """With one head the arrays of a call may differ in width."""
+    import torch
+    from kv_cache_compression_tma_b200 import ispa
+    k, kn = tensor((6, 1, 64), 1, torch.bfloat16), tensor((3, 1, 64), 2, torch.bfloat16)
+    lse, mass = torch.full((1, 3), 4.0, device="cuda"), torch.zeros((1, 9), device="cuda")
+    out = ispa.attn_mass(kn, k, lse, None, mass, mass_out=torch.zeros((1, 7), device="cuda"))
+    assert torch.equal(out[:, :6], ispa.attn_mass(kn, k, lse, None, mass)[:, :6])
+    pos = torch.arange(7, dtype=torch.int32, device="cuda")[None]
+    for m in (mass, mass[:, :6].clone()):  # the state back in place, rows of 9, 6 and 7
+        cache, want = k.clone(), k.clone()
+        m[0, :6] = torch.tensor([3.0, 0.0, 5.0, 1.0, 4.0, 2.0], device="cuda")
+        p = pos.clone()
+        assert ispa.cache_insert(cache, cache.clone(), m, p, 6, kn[:2], kn[:2], torch.full((1, 2), 9.0, device="cuda"), 6) == 6
+        want[1], want[3] = kn[0], kn[1]
+        assert torch.equal(cache, want) and p[0].tolist() == [0, 6, 2, 7, 4, 5, 6]
 
 
 def test_results_of_a_call_on_a_stream_come_from_its_memory(cuda_ok):
