@@ -170,6 +170,21 @@ def attn_args(ispa, **kw):
     return a
 
 
+def test_packed_attention_arguments_are_the_structure(ispa):
+    """Every field of the packed form lands where the structure has it."""
+    from kv_cache_compression_tma_b200 import ispa as mod
+    a, n, values = ispa.AttnArgs(), 0, []
+    for name, kind in a._fields_:
+        for i in range(getattr(kind, "_length_", 1)):
+            n += 1
+            values.append(n * 0.5 if kind is ctypes.c_float else n)
+            if hasattr(kind, "_length_"):
+                getattr(a, name)[i] = values[-1]
+            else:
+                setattr(a, name, values[-1])
+    assert mod._ATTN_ARGS.pack(*values) == bytes(a)
+
+
 def test_block_sparse_refusals(ispa):
     f = ispa.lib().ispa_block_sparse_attn
     call = lambda idx=P, n_sel=2, block=64, q_block=1, **kw: f(ctypes.byref(attn_args(ispa, **kw)), idx, n_sel, block, q_block, None)
