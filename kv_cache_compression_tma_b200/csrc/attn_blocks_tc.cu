@@ -20,6 +20,7 @@
 #include <string.h>
 
 #include "internal.h"
+#include "rows.cuh"
 #include "sm100.cuh"
 
 namespace ispa {
@@ -28,6 +29,8 @@ namespace {
 constexpr int kBM = 128;    // query rows per CTA
 constexpr int kBN = 128;    // keys per tile
 constexpr int kHalf = 64;   // keys per half
+constexpr int kSBufs = 3;   // S/P buffers
+constexpr int kTmemO = kSBufs * kBN;
 constexpr int kFirstSoftmaxWarp = 3;
 constexpr int kSoftmaxThreads = 256;
 constexpr int kThreads = 32 * kFirstSoftmaxWarp + kSoftmaxThreads;
@@ -38,7 +41,7 @@ struct Maps {
   CUtensorMap q;
   CUtensorMap k[3];    // sink, local: {64 cols, 128 rows}; history: {64 cols, 64 rows}
   CUtensorMap v[3];
-  CUtensorMap out[3];  // O_loc, O_full, D
+  CUtensorMap out[2];  // O_full, D
 };
 
 struct Params {
@@ -46,6 +49,9 @@ struct Params {
   int tiles[2];  // sink, local
   float scale_log2;
   bool want_d;
+  __nv_bfloat16* o_loc;
+  __nv_bfloat16* o_full;
+  int64_t ld_o;
   float* lse_loc;
   float* lse_hist;
   unsigned* status;
@@ -62,11 +68,12 @@ struct Cfg {
   static constexpr int kOffK = kOffQ + kTileBytes;
   static constexpr int kOffV = kOffK + 2 * kTileBytes;
   static constexpr int kOffBar = kOffV + 2 * kTileBytes;
-  // q_full, k_full[2], v_full[2], s_full[2], p_ready[2], o_done[2], o_final, final
-  static constexpr int kNumBars = 13;
+  // q_full, k_full[2], v_full[2], s_full[3], p_ready[3], o_done[2], m_ready[2], o_local, o_final, final
+  static constexpr int kNumBars = 18;
   static constexpr int kOffMisc = kOffBar + kNumBars * 8 + 8;
-  static constexpr int kOffMax = kOffMisc + 32;             // [3 slots][128 rows] row maxima
-  static constexpr int kOffList = kOffMax + 3 * kBM * 4;    // first key of each half
+  static constexpr int kOffSum = kOffMisc + 32;             // [group][128 rows] sums of a branch
+  static constexpr int kOffRun = kOffSum + 2 * kBM * 4;     // [tile % 2][128 rows] running maxima
+  static constexpr int kOffList = kOffRun + 2 * kBM * 4;    // first key of each half
   static constexpr uint32_t kIdescQK = idesc_bf16_f32(kBM, kBN, false, false);
   static constexpr uint32_t kIdescPV = idesc_bf16_f32(kBM, HD, false, true);
   static_assert(kOffList + 2 * kMaxSel * 4 <= 232448, "shared memory budget");
@@ -92,10 +99,12 @@ __global__ void __launch_bounds__(kThreads, 1) attn_blocks_tc_kernel(const __gri
   uint64_t* k_full = bars + 1;
   uint64_t* v_full = bars + 3;
   uint64_t* s_full = bars + 5;
-  uint64_t* p_ready = bars + 7;
-  uint64_t* o_done = bars + 9;
-  uint64_t* o_final = bars + 11;
-  uint64_t* final_bar = bars + 12;
+  uint64_t* p_ready = bars + 8;
+  uint64_t* o_done = bars + 11;
+  uint64_t* m_ready = bars + 13;
+  uint64_t* o_local = bars + 15;  // every tile of the local branch is in O
+  uint64_t* o_final = bars + 16;
+  uint64_t* final_bar = bars + 17;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::kOffMisc);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::kOffMisc + 4);
   volatile int* never = reinterpret_cast<volatile int*>(smem + C::kOffMisc + 8);  // stays 0: drain waits
@@ -112,10 +121,14 @@ __global__ void __launch_bounds__(kThreads, 1) attn_blocks_tc_kernel(const __gri
     for (int i = 0; i < 2; ++i) {
       mbar_init(k_full + i, 1);
       mbar_init(v_full + i, 1);
-      mbar_init(s_full + i, 1);
-      mbar_init(p_ready + i, kSoftmaxThreads / 32);
       mbar_init(o_done + i, 1);
+      mbar_init(m_ready + i, 4);
     }
+    for (int i = 0; i < kSBufs; ++i) {
+      mbar_init(s_full + i, 1);
+      mbar_init(p_ready + i, kSoftmaxThreads / 64);
+    }
+    mbar_init(o_local, 1);
     mbar_init(o_final, 1);
     mbar_init(final_bar, 1);
     *abort_flag = 0;
@@ -164,7 +177,6 @@ __global__ void __launch_bounds__(kThreads, 1) attn_blocks_tc_kernel(const __gri
     if (lane == 0) {
       const bool is_k = warp == 0;
       uint64_t* full = is_k ? k_full : v_full;
-      uint64_t* empty = is_k ? s_full : o_done;  // stage t % 2 frees with the MMA of tile t - 2
       if (is_k) {
         mbar_arrive_expect_tx(q_full, C::kTileBytes);
 #pragma unroll
@@ -174,7 +186,9 @@ __global__ void __launch_bounds__(kThreads, 1) attn_blocks_tc_kernel(const __gri
       int issued = 0;
       for (int t = 0; t < T; ++t) {
         const int s = t & 1;
-        if (t >= 2 && !mbar_wait(empty + s, ((t >> 1) - 1) & 1, abort_flag)) {
+        // stage t % 2 frees with the MMA of tile t - 2
+        if (t >= 2 && !(is_k ? mbar_wait(s_full + (t - 2) % kSBufs, ((t - 2) / kSBufs) & 1, abort_flag)
+                             : mbar_wait(o_done + s, ((t >> 1) - 1) & 1, abort_flag))) {
           atomicOr(p.status, kStatusTimeout);
           *abort_flag = 1;
           break;
@@ -211,42 +225,41 @@ __global__ void __launch_bounds__(kThreads, 1) attn_blocks_tc_kernel(const __gri
       bool ok = mbar_wait_warp(q_full, 0, abort_flag);
       tc_fence_after();
       const uint32_t q_base = smem_u32(smem + C::kOffQ);
-      auto issue_pv = [&](int u) -> bool {
-        const int b = u & 1;
-        if (!mbar_wait_warp(p_ready + b, (u >> 1) & 1, abort_flag)) return false;
-        if (!mbar_wait_warp(v_full + b, (u >> 1) & 1, abort_flag)) return false;
-        tc_fence_after();
-        const uint32_t o_tmem = tmem + 256 + (u >= T1 ? HD : 0);
-        const bool first = (u == 0) || (u == T1);
-        const uint32_t v_base = smem_u32(smem + C::kOffV + b * C::kTileBytes);
-#pragma unroll
-        for (int kk = 0; kk < kBN / 16; ++kk)
-          umma_ts_warp(o_tmem, tmem + b * 128 + kk * 8, sw128_desc(v_base + kk * 16 * 128, C::kBoxBytes, 1024), C::kIdescPV,
-                  (!first || kk > 0) ? 1u : 0u, leader);
-        umma_commit_warp(o_done + b, leader);
-        return true;
-      };
-      for (int t = 0; ok && t < T; ++t) {
-        const int s = t & 1;
-        if (!mbar_wait_warp(k_full + s, (t >> 1) & 1, abort_flag)) {
-          ok = false;
-          break;
-        }
+      auto issue_qk = [&](int t) -> bool {
+        const int s = t & 1, buf = t % kSBufs;  // the buffer is free: PV_{t-3} was issued before
+        if (!mbar_wait_warp(k_full + s, (t >> 1) & 1, abort_flag)) return false;
         tc_fence_after();
         const uint32_t k_base = smem_u32(smem + C::kOffK + s * C::kTileBytes);
 #pragma unroll
         for (int kk = 0; kk < HD / 16; ++kk) {
           const uint32_t off = (kk >> 2) * C::kBoxBytes + (kk & 3) * 32;
-          umma_ss_warp(tmem + s * 128, sw128_desc(q_base + off, 16, 1024), sw128_desc(k_base + off, 16, 1024), C::kIdescQK,
-                  kk > 0 ? 1u : 0u, leader);
+          umma_ss_warp(tmem + buf * kBN, sw128_desc(q_base + off, 16, 1024), sw128_desc(k_base + off, 16, 1024), C::kIdescQK,
+                       kk > 0 ? 1u : 0u, leader);
         }
-        umma_commit_warp(s_full + s, leader);
-        if (t > 0 && !issue_pv(t - 1)) {
-          ok = false;
-          break;
-        }
+        umma_commit_warp(s_full + buf, leader);
+        return true;
+      };
+      auto issue_pv = [&](int t) -> bool {
+        const int s = t & 1, buf = t % kSBufs;
+        if (!mbar_wait_warp(v_full + s, (t >> 1) & 1, abort_flag)) return false;
+        if (!mbar_wait_warp(p_ready + buf, (t / kSBufs) & 1, abort_flag)) return false;
+        tc_fence_after();
+        const bool first = t == 0 || t == T1;
+        const uint32_t v_base = smem_u32(smem + C::kOffV + s * C::kTileBytes);
+#pragma unroll
+        for (int kk = 0; kk < kBN / 16; ++kk)
+          umma_ts_warp(tmem + kTmemO, tmem + buf * kBN + kk * 8,
+                       sw128_desc(v_base + kk * 16 * 128, C::kBoxBytes, 1024), C::kIdescPV, (!first || kk > 0) ? 1u : 0u, leader);
+        umma_commit_warp(o_done + s, leader);
+        if (t == T1 - 1) umma_commit_warp(o_local, leader);
+        return true;
+      };
+      if (ok && T > 0) ok = issue_qk(0);
+      if (ok && T > 1) ok = issue_qk(1);
+      for (int t = 0; ok && t < T; ++t) {
+        if (t + 2 < T) ok = issue_qk(t + 2);
+        ok = ok && issue_pv(t);
       }
-      if (ok && T > 0) ok = issue_pv(T - 1);
       if (!ok) {
         if (leader) atomicOr(p.status, kStatusTimeout);
         *abort_flag = 1;
@@ -257,115 +270,168 @@ __global__ void __launch_bounds__(kThreads, 1) attn_blocks_tc_kernel(const __gri
     }
   } else {
     // ------------------------------------------------------------------ softmax + epilogue
-    const int quarter = warp & 3;                      // TMEM lane quarter this warp may access
-    const int part = (warp - kFirstSoftmaxWarp) >> 2;  // 64 key columns of S (HD/2 columns of O)
-    const int row = quarter * 32 + lane;               // query row within the tile == TMEM lane
+    const int quarter = warp & 3;                             // TMEM lane quarter this warp may access
+    const int group = (warp - kFirstSoftmaxWarp) >> 2;        // takes the tiles t % 2 == group
+    const int row = quarter * 32 + lane;                      // query row within the tile == TMEM lane
     const uint32_t lane_addr = static_cast<uint32_t>(quarter * 32) << 16;
-    // Row maxima of the key tiles: slot t % 3 collects tile t's maximum over the row's two threads by a
-    // shared-memory atomic max on order-preserving integer images; part 0 clears the slot of tile t-1
-    // after the barrier of tile t, ready for t+2.
-    int* mslot = reinterpret_cast<int*>(smem + C::kOffMax);
-    auto ordered = [](int i) { return i >= 0 ? i : i ^ 0x7fffffff; };  // an involution
-    const int kNegInf = ordered(__float_as_int(-INFINITY));
-    const int bar_id = 1 + quarter;  // named barrier of this row quarter's two warps
     const float sl2 = p.scale_log2;
-    constexpr int kCols = kBN / 2;   // S columns per thread: one half
-    constexpr int kOCols = HD / 2;   // O columns per thread
-    float m = -INFINITY, l = 0.f;    // l: partial row sum over this thread's columns
-    float m_loc = -INFINITY, l_loc = 0.f;
-    // A warp whose bounded wait ran out stops working but keeps executing one barrier per tile.
+    constexpr int kOCols = HD / 2;  // output columns per thread
+    float* sums = reinterpret_cast<float*>(smem + C::kOffSum);
+    float* running = reinterpret_cast<float*>(smem + C::kOffRun);
+    // m: the reference of this thread's partial sum l, the row's running maximum after the group's last tile
+    float m = -INFINITY, l = 0.f;
+    const bool has_hist = n_halves > 0;
+    // A warp whose bounded wait ran out stops working but keeps meeting the barriers.
     bool alive = true;
-    if (part == 0)
+
+    // The end of a branch whose last tile is `last`: every thread gets the row's (m, l), and O is complete.
+    float m_row, l_row;
+    auto join = [&](int last, uint64_t* done) {
+      if (alive) alive = mbar_wait_warp(done, 0, abort_flag);
+      asm volatile("bar.sync 1, %0;" ::"n"(kSoftmaxThreads) : "memory");  // every tile's maxima are read
+      m_row = running[(last & 1) * kBM + row];
+      sums[group * kBM + row] = m == m_row ? l : l * exp2f(m - m_row);
+      asm volatile("bar.sync 1, %0;" ::"n"(kSoftmaxThreads) : "memory");
+      l_row = sums[row] + sums[kBM + row];
+      tc_fence_after();
+    };
+    // 16 columns from c * 16 of this thread's part of the branch's output
+    const int o_col = group * kOCols;
+    auto output = [&](int c, float inv_l, float* o) {
+      uint32_t o0[16];
+      tmem_ld16(tmem + lane_addr + kTmemO + o_col + c * 16, o0);
+      tmem_wait_ld();
 #pragma unroll
-      for (int i = 0; i < 3; ++i) mslot[i * kBM + row] = kNegInf;
-    asm volatile("bar.sync %0, 64;" ::"r"(bar_id) : "memory");
-    uint32_t r[kCols];
-    for (int t = 0; t < T; ++t) {
-      const int b = t & 1;
-      int lim;  // how many of this thread's columns hold real keys
-      if (t < T1) {
-        const int seg = t < p.tiles[0] ? 0 : 1;
-        lim = p.n_kv[seg] - (t - (seg ? p.tiles[0] : 0)) * kBN - part * kCols;
-      } else {
-        lim = p.n_kv[2] - list[2 * (t - T1) + part];
-      }
-      if (t == T1) {  // branch switch: freeze the local branch, start the history branch
-        m_loc = m;
-        l_loc = l;
-        m = -INFINITY;
-        l = 0.f;
-      }
-      const bool first = (t == 0) || (t == T1);
-      if (alive) alive = mbar_wait_warp(s_full + b, (t >> 1) & 1, abort_flag);
-      const uint32_t s_addr = tmem + lane_addr + b * 128;
-      float mx = -INFINITY;
-      if (alive) {
-        tc_fence_after();
+      for (int j = 0; j < 16; ++j) o[j] = __uint_as_float(o0[j]) * inv_l;
+    };
+    const bool live_row = q0 + row < p.n_q;
+    const int64_t o_at = static_cast<int64_t>(q0 + row) * p.ld_o + head * HD + o_col;
+    auto pack8 = [](const float* v) {
+      return make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7]));
+    };
+    // O_loc rounded goes to its place; with a history, what the rounding left waits in O_full's place
+    auto store_local = [&]() {
+      const float inv_l = 1.f / l_row;
+#pragma unroll 1
+      for (int c = 0; c < kOCols / 16; ++c) {
+        float o[16];
+        output(c, inv_l, o);
+        if (!live_row) continue;
 #pragma unroll
-        for (int c = 0; c < kCols / 32; ++c) tmem_ld32(s_addr + part * kCols + c * 32, r + c * 32);
-        tmem_wait_ld();
-        if (lim >= kCols) {
-          float m8[kCols / 8];
+        for (int i = 0; i < 2; ++i) {
+          const uint4 hi = pack8(o + 8 * i);
+          *reinterpret_cast<uint4*>(p.o_loc + o_at + c * 16 + 8 * i) = hi;
+          if (has_hist) {
+            float h[8], lo[8];
+            unpack<__nv_bfloat16>(hi, h);
 #pragma unroll
-          for (int i = 0; i < kCols / 8; ++i) {
-            const float* v = reinterpret_cast<const float*>(r + 8 * i);
-            m8[i] = max3f(max3f(v[0], v[1], v[2]), max3f(v[3], v[4], v[5]), fmaxf(v[6], v[7]));
-          }
-          mx = max3f(max3f(m8[0], m8[1], m8[2]), max3f(m8[3], m8[4], m8[5]), fmaxf(m8[6], m8[7]));
-        } else {
-#pragma unroll
-          for (int j = 0; j < kCols; ++j) {
-            const float x = j < lim ? __uint_as_float(r[j]) : -INFINITY;
-            r[j] = __float_as_uint(x);
-            mx = fmaxf(mx, x);
+            for (int j = 0; j < 8; ++j) lo[j] = isinf(h[j]) ? 0.f : o[8 * i + j] - h[j];
+            *reinterpret_cast<uint4*>(p.o_full + o_at + c * 16 + 8 * i) = pack8(lo);
           }
         }
       }
-      const int slot = (t % 3) * kBM + row;
-      atomicMax(mslot + slot, ordered(__float_as_int(mx)));
-      asm volatile("bar.sync %0, 64;" ::"r"(bar_id) : "memory");
-      mx = __int_as_float(ordered(mslot[slot])) * sl2;
-      if (part == 0) mslot[((t + 2) % 3) * kBM + row] = kNegInf;
+    };
+
+    float lse_loc2 = 0.f;  // in log2 units
+    bool in_hist = false;
+    for (int t = group;; t += 2) {
+      if (has_hist && !in_hist && t >= T1) {  // branch switch: set the local branch aside, both groups together
+        in_hist = true;
+        join(T1 - 1, o_local);
+        if (alive) {
+          lse_loc2 = m_row + __log2f(l_row);
+          store_local();
+          tc_fence_before();
+        }
+        asm volatile("bar.sync 1, %0;" ::"n"(kSoftmaxThreads) : "memory");  // O may be overwritten
+        m = -INFINITY;
+        l = 0.f;
+      }
+      if (t >= T) break;
+      const uint32_t s_addr = tmem + lane_addr + t % kSBufs * kBN;
+      int lim[2];  // how many of each half's columns hold real keys
+      if (t < T1) {
+        const int seg = t < p.tiles[0] ? 0 : 1;
+        lim[0] = p.n_kv[seg] - (t - (seg ? p.tiles[0] : 0)) * kBN;
+        lim[1] = lim[0] - kHalf;
+      } else {
+        lim[0] = p.n_kv[2] - list[2 * (t - T1)];
+        lim[1] = p.n_kv[2] - list[2 * (t - T1) + 1];
+      }
+      if (alive) alive = mbar_wait_warp(s_full + t % kSBufs, (t / kSBufs) & 1, abort_flag);
       if (!alive) continue;
-      bool rescale = false;
-      float alpha = 1.f;
-      if (first) {
-        m = mx;
-      } else if (mx > m + kRescaleThreshold) {
-        alpha = fast_exp2(m - mx);
-        m = mx;
-        rescale = true;
+      tc_fence_after();
+      uint32_t r[kBN];
+#pragma unroll
+      for (int c = 0; c < kBN / 32; ++c) tmem_ld32(s_addr + c * 32, r + c * 32);
+      tmem_wait_ld();
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+        if (lim[h] < kHalf) {
+#pragma unroll
+          for (int j = 0; j < kHalf; ++j)
+            if (j >= lim[h]) r[h * kHalf + j] = __float_as_uint(-INFINITY);
+        }
+      float m16[kBN / 8];
+#pragma unroll
+      for (int i = 0; i < kBN / 8; ++i) {
+        const float* v = reinterpret_cast<const float*>(r + 8 * i);
+        m16[i] = max3f(max3f(v[0], v[1], v[2]), max3f(v[3], v[4], v[5]), fmaxf(v[6], v[7]));
+      }
+#pragma unroll
+      for (int i = 0; i < 5; ++i) m16[i] = max3f(m16[i], m16[i + 5], m16[i + 10]);
+      const float top = fmaxf(max3f(m16[0], m16[1], m16[2]), max3f(m16[3], m16[4], m16[15])) * sl2;
+      // the running maximum after the other group's last tile
+      float m_prev = -INFINITY;
+      if (t != 0 && t != T1) {
+        alive = mbar_wait_warp(m_ready + ((t - 1) & 1), ((t - 1) >> 1) & 1, abort_flag);
+        m_prev = running[((t - 1) & 1) * kBM + row];
+      }
+      const float m_new = m_prev == -INFINITY || top > m_prev + kRescaleThreshold ? top : m_prev;
+      running[(t & 1) * kBM + row] = m_new;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(m_ready + (t & 1));
+      if (!alive) continue;
+      const bool rescale = m_new != m_prev && m_prev != -INFINITY;
+      if (m != m_new) {  // m = -inf: nothing to scale yet
+        l *= fast_exp2(m - m_new);
+        m = m_new;
       }
       const float neg_m = m == -INFINITY ? 0.f : -m;  // a row whose keys so far all score -inf: weights 0
       const uint64_t sl2x2 = pack_f2(sl2, sl2), negm2 = pack_f2(neg_m, neg_m);
       uint64_t acc[4] = {0ull, 0ull, 0ull, 0ull};
-      uint32_t pk[kCols / 2];
 #pragma unroll
-      for (int j = 0; j < kCols; j += 2) {
-        const uint64_t y = fma_f2(pack_f2(__uint_as_float(r[j]), __uint_as_float(r[j + 1])), sl2x2, negm2);
-        float y0, y1;
-        unpack_f2(y, y0, y1);
-        const float p0 = fast_exp2(y0), p1 = fast_exp2(y1);
-        acc[(j >> 1) & 3] = add_f2(acc[(j >> 1) & 3], pack_f2(p0, p1));
-        pk[j >> 1] = pack_bf16x2(p0, p1);
+      for (int h = 0; h < 2; ++h) {
+        uint32_t pk[kHalf / 2];
+#pragma unroll
+        for (int j = 0; j < kHalf; j += 2) {
+          const int x = h * kHalf + j;
+          const uint64_t y = fma_f2(pack_f2(__uint_as_float(r[x]), __uint_as_float(r[x + 1])), sl2x2, negm2);
+          float y0, y1;
+          unpack_f2(y, y0, y1);
+          const float p0 = fast_exp2(y0), p1 = fast_exp2(y1);
+          acc[(j >> 1) & 3] = add_f2(acc[(j >> 1) & 3], pack_f2(p0, p1));
+          pk[j >> 1] = pack_bf16x2(p0, p1);
+        }
+        tmem_st32(s_addr + h * (kHalf / 2), pk);  // over S, read by now
       }
       float a0, a1, a2, a3, a4, a5, a6, a7;
       unpack_f2(acc[0], a0, a1);
       unpack_f2(acc[1], a2, a3);
       unpack_f2(acc[2], a4, a5);
       unpack_f2(acc[3], a6, a7);
-      l = l * alpha + (((a0 + a1) + (a2 + a3)) + ((a4 + a5) + (a6 + a7)));
-      tmem_st32(s_addr + part * (kCols / 2), pk);
+      l += ((a0 + a1) + (a2 + a3)) + ((a4 + a5) + (a6 + a7));
       // The warp rescales together if any of its rows needs it; only then must PV_{t-1} be complete.
-      // S_t complete implies PV_{t-2} complete, so the parity wait on o_done[(t-1) % 2] cannot alias.
+      // S_t complete implies PV_{t-3} complete, so the parity wait on o_done cannot alias.
       const bool any = __any_sync(0xffffffffu, rescale);
-      if (any && t > 0) alive = mbar_wait_warp(o_done + ((t - 1) & 1), ((t - 1) >> 1) & 1, abort_flag);
+      if (any) alive = mbar_wait_warp(o_done + ((t - 1) & 1), ((t - 1) >> 1) & 1, abort_flag);
       if (!alive) continue;
       if (any) {
         tc_fence_after();
-        const uint32_t o_addr = tmem + lane_addr + 256 + (t >= T1 ? HD : 0) + part * kOCols;
-#pragma unroll
-        for (int c = 0; c < kOCols / 32; ++c) {
+        const float alpha = rescale ? fast_exp2(m_prev - m_new) : 1.f;
+        const uint32_t o_addr = tmem + lane_addr + kTmemO;
+#pragma unroll 1
+        for (int c = 0; c < HD / 32; ++c) {
           uint32_t o[32];
           tmem_ld32(o_addr + c * 32, o);
           tmem_wait_ld();
@@ -377,83 +443,75 @@ __global__ void __launch_bounds__(kThreads, 1) attn_blocks_tc_kernel(const __gri
       tmem_wait_st();
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(p_ready + b);
+      if (lane == 0) mbar_arrive(p_ready + t % kSBufs);
     }
-    if (alive) alive = mbar_wait_warp(o_final, 0, abort_flag);
-    // Partial row sums exchanged through the K ring: o_final has seen every MMA complete, and every load
-    // the MMAs waited for, so no copy or MMA touches the ring any more.
-    float* xchg = reinterpret_cast<float*>(smem + C::kOffK);
-    const bool has_hist = n_halves > 0;
-    if (!has_hist) {
-      m_loc = m;
-      l_loc = l;
-    }
-    xchg[part * kBM + row] = l_loc;
-    xchg[(2 + part) * kBM + row] = l;
-    asm volatile("bar.sync %0, 64;" ::"r"(bar_id) : "memory");
-    const float l_loc_row = xchg[row] + xchg[kBM + row], l_hist_row = xchg[2 * kBM + row] + xchg[3 * kBM + row];
-    // staging tile of output w (0 O_loc, 1 O_full, 2 D) in the idle rings
-    auto stage = [&](int w) -> uint8_t* {
-      return w < 2 ? smem + C::kOffV + w * C::kTileBytes : smem + C::kOffK + C::kTileBytes;
-    };
+    join(T - 1, o_final);
+    // staging tile of output w (0 O_full, 1 D) in the idle V ring: o_final has seen every MMA complete, and
+    // every load the MMAs waited for
+    auto stage = [&](int w) -> uint8_t* { return smem + C::kOffV + w * C::kTileBytes; };
     if (!alive) {
       atomicOr(p.status, kStatusTimeout);
       *abort_flag = 1;
     } else {
-      tc_fence_after();
-      const float lse_loc2 = m_loc + __log2f(l_loc_row);
-      const float lse_hist2 = has_hist ? m + __log2f(l_hist_row) : -INFINITY;
+      const float lse2 = m_row + __log2f(l_row);
       float w_loc = 1.f, w_hist = 0.f;
       if (has_hist) {
-        const float mm = fmaxf(lse_loc2, lse_hist2);
-        const float a = exp2f(lse_loc2 - mm), bb = exp2f(lse_hist2 - mm);
+        const float mm = fmaxf(lse_loc2, lse2);
+        const float a = exp2f(lse_loc2 - mm), bb = exp2f(lse2 - mm);
         w_loc = a / (a + bb);
         w_hist = bb / (a + bb);
+      } else {
+        lse_loc2 = lse2;
+        store_local();
       }
-      const float inv_l_loc = 1.f / l_loc_row;
-      const float inv_l_hist = has_hist && l_hist_row != 0.f ? 1.f / l_hist_row : 0.f;
-      const uint32_t oa_addr = tmem + lane_addr + 256 + part * kOCols;
+      const float inv_l = l_row != 0.f ? 1.f / l_row : 0.f;
       auto put = [&](int which, int col, const float* v8) {  // 8 values at tile column col, 128-byte swizzle
-        uint4 w;
-        w.x = pack_bf16x2(v8[0], v8[1]);
-        w.y = pack_bf16x2(v8[2], v8[3]);
-        w.z = pack_bf16x2(v8[4], v8[5]);
-        w.w = pack_bf16x2(v8[6], v8[7]);
-        *reinterpret_cast<uint4*>(stage(which) + (col >> 6) * C::kBoxBytes + row * 128 + ((((col & 63) >> 3) ^ (row & 7)) << 4)) = w;
+        *reinterpret_cast<uint4*>(stage(which) + (col >> 6) * C::kBoxBytes + row * 128 + ((((col & 63) >> 3) ^ (row & 7)) << 4)) =
+            pack8(v8);
       };
 #pragma unroll 1
-      for (int c = 0; c < kOCols / 32; ++c) {
-        uint32_t oa[32], ob[32];
-        tmem_ld32(oa_addr + c * 32, oa);
-        if (has_hist) tmem_ld32(oa_addr + HD + c * 32, ob);
-        tmem_wait_ld();
+      for (int c = 0; c < kOCols / 16; ++c) {
+        float o[16];
+        output(c, has_hist ? inv_l : 1.f / l_row, o);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          float vl[8], vf[8], vd[8];
+        for (int i = 0; i < 2; ++i) {
+          float vf[8], vd[8];
+          if (has_hist) {
+            float vl[8], lo[8];
+            const int64_t at = o_at + c * 16 + 8 * i;
+            const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
+            unpack<__nv_bfloat16>(live_row ? *reinterpret_cast<const uint4*>(p.o_loc + at) : zero, vl);
+            unpack<__nv_bfloat16>(live_row ? *reinterpret_cast<const uint4*>(p.o_full + at) : zero, lo);
 #pragma unroll
-          for (int j = 0; j < 8; ++j) {
-            vl[j] = __uint_as_float(oa[8 * i + j]) * inv_l_loc;
-            vf[j] = has_hist ? fmaf(w_loc, vl[j], w_hist * (__uint_as_float(ob[8 * i + j]) * inv_l_hist)) : vl[j];
-            vd[j] = vf[j] - vl[j];
+            for (int j = 0; j < 8; ++j) {
+              vl[j] += lo[j];
+              vf[j] = fmaf(w_loc, vl[j], w_hist * o[8 * i + j]);
+              vd[j] = vf[j] - vl[j];
+            }
+          } else {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+              vf[j] = o[8 * i + j];
+              vd[j] = vf[j] - vf[j];
+            }
           }
-          const int col = part * kOCols + c * 32 + 8 * i;
-          put(0, col, vl);
-          put(1, col, vf);
-          if (p.want_d) put(2, col, vd);
+          const int col = o_col + c * 16 + 8 * i;
+          put(0, col, vf);
+          if (p.want_d) put(1, col, vd);
         }
       }
-      if (q0 + row < p.n_q && part == 0) {
+      if (live_row && group == 0) {
         const float ln2 = 0.69314718055994531f;
         const int64_t at = static_cast<int64_t>(head) * p.n_q + q0 + row;
         p.lse_loc[at] = lse_loc2 * ln2;
-        p.lse_hist[at] = has_hist ? lse_hist2 * ln2 : -INFINITY;
+        p.lse_hist[at] = has_hist ? lse2 * ln2 : -INFINITY;
       }
-      asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+      asm volatile("fence.proxy.async;" ::: "memory");  // of the staging tiles, and of O_full's place in memory
     }
     // every softmax thread has staged its part (or the CTA gave up); one thread stores the tiles
-    asm volatile("bar.sync 5, %0;" ::"n"(kSoftmaxThreads) : "memory");
+    asm volatile("bar.sync 1, %0;" ::"n"(kSoftmaxThreads) : "memory");
     if (warp == kFirstSoftmaxWarp && lane == 0 && !*abort_flag) {
-      for (int w = 0; w < (p.want_d ? 3 : 2); ++w)
+      for (int w = 0; w < (p.want_d ? 2 : 1); ++w)
         for (int b = 0; b < C::kBoxes; ++b) store_tile_2d(&maps.out[w], stage(w) + b * C::kBoxBytes, head * HD + 64 * b, q0);
       asm volatile("cp.async.bulk.commit_group;" ::: "memory");
       asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
@@ -485,13 +543,15 @@ cudaError_t launch_hd(const AttnLaunch& a, const BlockList& b, cudaStream_t stre
     ok = ok && make_map_bf16_2d(&maps.k[s], a.k[s], a.n_kv[s], d, a.ld_k[s], 64, box) &&
          make_map_bf16_2d(&maps.v[s], a.v[s], a.n_kv[s], d, a.ld_v[s], 64, box);
   }
-  ok = ok && make_map_bf16_2d(&maps.out[0], a.o_loc, a.n_q, d, a.ld_o, 64, kBM) &&
-       make_map_bf16_2d(&maps.out[1], a.o_full, a.n_q, d, a.ld_o, 64, kBM) &&
-       (!a.d_out || make_map_bf16_2d(&maps.out[2], a.d_out, a.n_q, d, a.ld_o, 64, kBM));
+  ok = ok && make_map_bf16_2d(&maps.out[0], a.o_full, a.n_q, d, a.ld_o, 64, kBM) &&
+       (!a.d_out || make_map_bf16_2d(&maps.out[1], a.d_out, a.n_q, d, a.ld_o, 64, kBM));
   if (!ok) return cudaErrorInvalidValue;
   p.n_q = static_cast<int>(a.n_q);
   p.scale_log2 = a.scale * 1.4426950408889634f;
   p.want_d = a.d_out != nullptr;
+  p.o_loc = static_cast<__nv_bfloat16*>(a.o_loc);
+  p.o_full = static_cast<__nv_bfloat16*>(a.o_full);
+  p.ld_o = a.ld_o;
   p.lse_loc = a.lse_loc;
   p.lse_hist = a.lse_hist;
   p.status = a.status;
