@@ -47,10 +47,10 @@ void count(int n) { g_launches.fetch_add(static_cast<uint64_t>(n)); }
 
 bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
 
-// Up to this many (query, head) rows, block-sparse attention of whole row groups takes the row kernel:
-// 80 rows of 40 heads 46 us against 65 on the tensor cores, 96 of 12 heads 73 against 103, but 160 of
-// 40 heads 89 against 65 (each row reads its keys for itself).
-constexpr int64_t kBlockRowsMax = 96;
+// Up to this many (query, head) rows, block-sparse attention of whole row groups takes the row kernel, one
+// CTA per row and SM: over 7216 keys 27 us for 40 rows, 49 for 80 to 144, against 55 to 57 on the tensor
+// cores; at 160 rows a second wave makes it 96 (each row reads its keys for itself).
+constexpr int64_t kBlockRowsMax = 148;
 
 // Heads of the bounded-history calls: one grid dimension of 65535 covers a row's 256-byte pieces at any
 // head_dim and type.

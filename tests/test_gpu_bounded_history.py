@@ -325,6 +325,8 @@ def test_sparse_rows_fp32(cuda_ok, H, hd, n_q, q_block, n_sink, n_loc, n_hist, b
     (1, 64, 1, 128, 0, 1, 1, 64, 1), (2, 128, 300, 128, 40, 300, 1000, 64, 5), (2, 128, 257, 128, 0, 130, 777, 128, 3),
     (2, 64, 128, 128, 10, 0, 300, 64, 9), (1, 128, 700, 256, 128, 256, 4000, 128, 33), (3, 64, 130, 384, 1, 1, 63, 128, 2),
     (1, 128, 129, 128, 0, 64, 192, 128, 2), (2, 128, 48, 128, 5, 64, 192, 64, 2), (2, 128, 49, 128, 5, 64, 192, 64, 2),
+    (2, 128, 74, 128, 5, 64, 192, 64, 2), (2, 128, 75, 128, 5, 64, 192, 64, 2), (1, 64, 149, 128, 0, 128, 100, 64, 1),
+    (2, 128, 128, 128, 0, 129, 129, 128, 2), (1, 128, 400, 128, 100, 400, 5000, 128, 40),
 ])
 @pytest.mark.parametrize("pad", [0, 8])
 def test_sparse_tensor_cores(cuda_ok, H, hd, n_q, q_block, n_sink, n_loc, n_hist, block, n_sel, pad):
@@ -352,6 +354,30 @@ def test_sparse_tensor_cores_odd_lists_and_dense_limit(cuda_ok):
         with pytest.raises(ispa.IspaError) as e:
             ispa.block_sparse_attn(*t.values(), idx[:, :, :1].contiguous(), block=96, q_block=128)
         assert e.value.status == ispa.ISPA_ERR_UNSUPPORTED
+
+
+def test_sparse_longest_list(cuda_ok):
+    """4096 entries of blocks of 128: three blocks, the last one ragged, 1365 times each.  O_hist is that of the
+    three alone and lse_hist larger by log 1365.  Beside the usual tolerances: l is the sum of 1707 tiles'
+    sums per group, each rounded by at most 2^-24 of it; O takes 8 products per tile of 3413, each
+    truncated by at most 2^-23 of it."""
+    import torch
+    from kv_cache_compression_tma_b200 import ispa
+    t, _ = sparse_case("bf16", 1, 128, 160, 128, 4, 30, 300, 128, 1, 70)
+    idx = torch.tensor(([0, 1, 2] * 1366)[:4095] + [-1], dtype=torch.int32, device="cuda").repeat(1, 2, 1)
+    out = ispa.block_sparse_attn(*t.values(), idx, block=128, q_block=128)
+    assert ispa.get_device_status() == ispa.ISPA_OK
+    ref = orc.block_sparse(*(host(x) for x in t.values()), idx[:, :, :3].cpu().numpy(), 128, 128)
+    share = lambda lh: (1.0 / (1.0 + np.exp(ref["lse_loc"] - lh))).T[:, :, None]
+    o_hist = ref["O_loc"] + (ref["O_full"] - ref["O_loc"]) / share(ref["lse_hist"])
+    lse_hist = ref["lse_hist"] + np.log(1365.0)
+    o_full = ref["O_loc"] + share(lse_hist) * (o_hist - ref["O_loc"])
+    extra_l, extra_o = 1707 * 2.0 ** -24, 3413 * 8 * 2.0 ** -23
+    assert np.max(np.abs(host(out["lse_hist"]) - lse_hist)) <= ATTN_TOL["lse_hist"] + extra_l
+    assert rel(host(out["o_loc"]), ref["O_loc"].reshape(160, -1)) <= ATTN_TOL["o_loc"]
+    for w, want in (("o_full", o_full), ("d", o_full - ref["O_loc"])):
+        big = np.linalg.norm(o_hist) / np.linalg.norm(want)
+        assert rel(host(out[w]), want.reshape(160, -1)) <= ATTN_TOL[w] + (extra_l + extra_o) * big, w
 
 
 def test_sparse_odd_lists(cuda_ok):
@@ -393,7 +419,8 @@ def test_sparse_empty_history_and_no_queries(cuda_ok, dtype, n_q, q_block, n_his
         assert ispa.block_sparse_attn(*t.values(), idx, block=64, q_block=q_block)["o_loc"].shape == (0, 128)
 
 
-@pytest.mark.parametrize("dtype,n_q,q_block,block", [("bf16", 2, 1, 64), ("fp32", 2, 1, 64), ("bf16", 130, 128, 64), ("bf16", 130, 128, 128)])
+@pytest.mark.parametrize("dtype,n_q,q_block,block", [("bf16", 2, 1, 64), ("fp32", 2, 1, 64), ("bf16", 130, 128, 64), ("bf16", 130, 128, 128),
+                                                     ("bf16", 150, 128, 64), ("bf16", 200, 128, 128)])
 def test_sparse_keys_that_score_minus_infinity(cuda_ok, dtype, n_q, q_block, block):
     """Keys whose products overflow to -inf (the first ones of a branch, too) weigh nothing; a history of
     nothing else gives lse_hist = -inf and O_full = O_loc."""
