@@ -1,20 +1,33 @@
 // attn_blocks_tc.cu -- dual-stream attention over sink, local and selected history blocks on tcgen05
 // tensor cores: one CTA per (128 query rows, head), whose rows share one list of history blocks.
 //
-// The algorithm is the dense dual-stream kernel's: keys are walked once in tiles of 128, local branch
-// first, an online softmax (m, l, fp32 accumulator in TMEM) per branch, and
+// Keys are walked once in tiles of 128, local branch first, with an online softmax (m, l, fp32
+// accumulator in TMEM) per branch, and
 //   O_loc = O_A / l_loc,  O_full = w_loc O_loc + w_hist O_B / l_hist,  D = O_full - O_loc.
-// What differs is where a history tile comes from.  The CTA first turns its list into halves of 64
-// keys (a block is one or two of them; entries that name no block, and empty halves of the history's
-// last block, are dropped), and a history tile is any two consecutive halves: two 64-row TMA boxes per
-// 64 columns instead of one 128-row box.  So both block sizes fill whole MMA tiles, and a ragged block
-// may lie anywhere in the list.  Softmax thread part p of a row owns half p's columns, so each half's
-// count of real keys masks exactly one thread's columns.
+// The CTA first turns its list into halves of 64 keys (a block is one or two of them; entries that name
+// no block, and empty halves of the history's last block, are dropped), and a history tile is any two
+// consecutive halves: two 64-row TMA boxes per 64 columns instead of one 128-row box.  So both block
+// sizes fill whole MMA tiles, and a ragged block may lie anywhere in the list.
 //
-// Warp roles (352 threads): warp 0 Q and the K ring, warp 2 the V ring, warp 1 TMEM and the MMAs
-// (S_t = Q K_t^T into S buffer t%2; O += P_t V_t with P_t read from TMEM), warps 3..10 softmax and
-// epilogue, two threads per row.  Two commits per tile: s_full[t%2] (also frees K_t), o_done[t%2] (also
-// frees V_t).  TMEM columns: [0,256) two S/P buffers, [256,256+HD) O_A, then O_B.
+// Two groups of four softmax warps, a query row per thread, take the tiles by turns, so that one forms
+// its maximum or waits while the other keeps the exponentials going.  Both scale by one running maximum per
+// row, which a group reads after the other's last tile and hands on (m_ready); each keeps a partial
+// sum of its own.  S runs two tiles ahead of P V in three TMEM buffers.  That leaves one accumulator: at
+// the branch switch O_loc goes to its place in memory, rounded, and what the rounding left goes to
+// O_full's place, where the same thread finds it again for the epilogue (together 16 bits of O_loc).
+//
+// Bound: the loop of three tiles (softmax of one, P V and the S that waits for its buffer) at about 1430
+// clocks per tile (1024 of MMA), and power.  12 heads x 4680 queries over 6240 local keys and 64 blocks of
+// 128 (415 GFLOP, 0.254 ms at the measured bf16 peak): 0.39 ms alone, tensor pipe 59 % busy, 0.46 ms back
+// to back at 995 W.  Measured beside it: two threads per row and one group on two S buffers, a second
+// accumulator (2090 clocks, 0.49 ms); two groups with accumulators of their own on two S buffers (the
+// same); two threads per row here (0.467 against 0.452); S read a second time instead of held in
+// registers (0.50); the two products issued by two warps (their operands alternate: 10 % slower);
+// three V stages and polynomial exponentials (nothing, and slower).
+//
+// Warp roles (352 threads): warp 0 Q and the K ring, warp 2 the V ring, warp 1 TMEM and the MMAs, warps
+// 3..10 softmax and epilogue.  Commits: s_full[t%3] (also frees K_t), o_done[t%2] (also frees V_t).
+// TMEM columns: [0,384) three S/P buffers (P_t over the first half of S_t), [384,384+HD) O.
 // Every barrier wait is bounded (sm100.cuh); one that runs out records ISPA_ERR_TIMEOUT and unwinds.
 #include <math.h>
 #include <string.h>
