@@ -203,11 +203,19 @@ def _heads_rows(t, what: str, H: int, hd: int, dtype, device: int, n: Optional[i
     return shape[0], stride[0] if shape[0] > 1 else H * hd
 
 
+INT32_MAX = 2 ** 31 - 1
+
+
+def _int32(x: int, what: str, low: int = -2 ** 31) -> int:
+    """x as the ABI's int32: ctypes would drop the high bits of a larger one without a word."""
+    if not low <= x <= INT32_MAX:
+        raise ValueError(f"{what} must lie in {low} .. 2^31 - 1")
+    return x
+
+
 def _pieces(n: int, size: int, what: str) -> int:
     """How many pieces of `size` cover n."""
-    if size < 1:
-        raise ValueError(f"{what} must be at least 1")
-    return -(-n // size)
+    return -(-n // _int32(size, what, 1))
 
 
 def _state_rows(t, what: str, H: int, cols: int, dtype, device: int) -> int:
@@ -483,9 +491,6 @@ def attn_mass(q, k, lse_loc, lse_hist, mass, *, kv_bias=None, decay: float = 1.0
     return mass_out
 
 
-INT32_MAX = 2 ** 31 - 1
-
-
 def cache_insert(k_cache, v_cache, mass, pos, n: int, k_new, v_new, mass_new, pos_new: int, *, keep_below: int = 0,
                  keep_from: int = INT32_MAX, mass_out=None, pos_out=None, stream=None) -> int:
     """ispa_cache_insert: the new tokens k_new, v_new [n_new, H, hd] with weights mass_new (fp32 [H, n_new],
@@ -521,7 +526,8 @@ def cache_insert(k_cache, v_cache, mass, pos, n: int, k_new, v_new, mass_new, po
     mn, ld_mn = (None, 0) if mass_new is None else (mass_new.data_ptr(), _state_rows(mass_new, "mass_new", H, n_new, f32, dev))
     _check(lib().ispa_cache_insert(_dtype_code(k_cache), H, hd, k_cache.data_ptr(), v_cache.data_ptr(), ld_cache, capacity,
                                    n, mass.data_ptr(), pos.data_ptr(), ld_state, k_new.data_ptr(), v_new.data_ptr(),
-                                   n_new, ld_new, mn, ld_mn, pos_new, keep_below, keep_from, mass_out.data_ptr(),
+                                   n_new, ld_new, mn, ld_mn, _int32(pos_new, "pos_new"), _int32(keep_below, "keep_below"),
+                                   _int32(keep_from, "keep_from"), mass_out.data_ptr(),
                                    pos_out.data_ptr(), ld_out, _stream(stream)), "ispa_cache_insert")
     return total
 
@@ -572,6 +578,7 @@ def block_means(k, means, block: int, *, first: int = 0, stream=None):
     rows, ld_means = _heads_rows(means, "means", H, hd, torch.float32, dev)
     if rows < _pieces(n_k, block, "block"):
         raise ValueError("means has fewer rows than k has blocks")
+    _int32(first, "first", 0)
     _check(lib().ispa_block_means(_dtype_code(k), H, hd, k.data_ptr(), n_k, ld_k, block, first, means.data_ptr(),
                                   ld_means, _stream(stream)), "ispa_block_means")
     return means
@@ -590,7 +597,7 @@ def block_select(q, means, n_sel: int, *, q_block: int = 1, out=None, stream=Non
         with _alloc_on(stream):
             out = torch.empty(shape, dtype=torch.int32, device=q.device)
     _check(lib().ispa_block_select(_dtype_code(q), H, hd, q.data_ptr(), n_q, ld_q, q_block, means.data_ptr(), n_blocks,
-                                   ld_means, n_sel, _dense(out, "out", shape, torch.int32, dev), _stream(stream)),
+                                   ld_means, _int32(n_sel, "n_sel"), _dense(out, "out", shape, torch.int32, dev), _stream(stream)),
            "ispa_block_select")
     return out
 
@@ -657,7 +664,7 @@ def block_sparse_attn(q, k_sink, v_sink, k_loc, v_loc, k_hist, v_hist, idx, *, b
             raise ValueError(f"outputs must be {dtype} {list(shape)} with one row stride")
         if o.get_device() != dev:
             _on_current_device(o)
-    n_sel, groups = idx.shape[-1], _pieces(n_q, q_block, "q_block")
+    n_sel, groups = _int32(idx.shape[-1], "n_sel"), _pieces(n_q, q_block, "q_block")
     a = _ATTN_ARGS.pack(_dtype_code(q), H, hd, ISPA_ATTN_CUDA_CORES if cuda_cores else 0, n_q, ns, nl, nh, q.data_ptr(), ld_q,
                         k_sink.data_ptr(), k_loc.data_ptr(), k_hist.data_ptr(),
                         v_sink.data_ptr(), v_loc.data_ptr(), v_hist.data_ptr(), ld_ks, ld_kl, ld_kh, ld_vs, ld_vl, ld_vh,
@@ -665,7 +672,7 @@ def block_sparse_attn(q, k_sink, v_sink, k_loc, v_loc, k_hist, v_hist, idx, *, b
                         _dense(lse_loc, "lse_loc", (H, n_q), f32, dev), _dense(lse_hist, "lse_hist", (H, n_q), f32, dev),
                         0 if d_out is None else d_out.data_ptr(), 0, 0, 0, 0, 0, 0)
     _check(lib().ispa_block_sparse_attn(a, _dense(idx, "idx", (H, groups, n_sel), torch.int32, dev),
-                                        n_sel, block, q_block, _stream(stream)), "ispa_block_sparse_attn")
+                                        n_sel, _int32(block, "block"), q_block, _stream(stream)), "ispa_block_sparse_attn")
     return {"o_loc": o_loc, "o_full": o_full, "d": d_out, "lse_loc": lse_loc, "lse_hist": lse_hist}
 
 

@@ -202,3 +202,39 @@ def test_block_sparse_refusals(ispa):
     assert f(ctypes.byref(a), P, 2, 64, 1, None) == 1            # empty local branch
     assert call(n_q=0) == 0
     assert ispa.launch_count() == n0
+
+
+# ------------------------------------------------------------------------------------------ the binding
+def test_sizes_past_the_abis_integers_are_refused(monkeypatch):
+    """ctypes drops the high bits of an integer: a block of 2^32 + 1 tokens would pass the binding's shape
+    checks and reach the library as one of 1.  On host tensors with the library faked: no call gets through."""
+    import torch
+    from kv_cache_compression_tma_b200 import ispa
+
+    class Library:
+        def __getattr__(self, name):
+            return lambda *a: pytest.fail(f"{name} was called")
+
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: -1)  # what get_device() says of a host tensor
+    monkeypatch.setattr(ispa, "lib", Library)
+    monkeypatch.setattr(ispa, "_stream", lambda stream: 0)
+    k, means = torch.zeros((8, 2, 64)), torch.zeros((8, 2, 64))
+    mass, pos = torch.zeros((2, 8)), torch.zeros((2, 8), dtype=torch.int32)
+    idx = torch.zeros((2, 1, 1), dtype=torch.int32)
+    wrap = 2 ** 32 + 1
+    insert = lambda pos_new=8, **kw: ispa.cache_insert(k, k, mass, pos, 8, k, k, None, pos_new, **kw)
+    sparse = lambda **kw: ispa.block_sparse_attn(k, k, k, k, k, k, k, idx, **kw)
+    bad = [lambda: ispa.block_means(k, means, wrap), lambda: ispa.block_means(k, means, 4, first=2 ** 64),
+           lambda: ispa.block_means(k, means, 4, first=-1), lambda: ispa.block_select(k, means, 1, q_block=wrap),
+           lambda: ispa.block_select(k, means, wrap, out=idx.expand(2, 8, 1)), lambda: sparse(block=wrap, q_block=8),
+           lambda: sparse(block=4, q_block=wrap), lambda: insert(keep_from=2 ** 31), lambda: insert(keep_from=2 ** 32),
+           lambda: insert(keep_below=2 ** 31), lambda: insert(keep_below=-2 ** 31 - 1), lambda: insert(pos_new=wrap)]
+    for call in bad:
+        with pytest.raises(ValueError):
+            call()
+    cache = ispa.MassCache(2, 64, 8, dtype=torch.float32, device="cpu")
+    cache.seen = 2 ** 31
+    for kw in ({}, {"recent": 4}):
+        with pytest.raises(ValueError):
+            cache.insert(k, k, **kw)
+    assert cache.seen == 2 ** 31 and cache.n == 0
