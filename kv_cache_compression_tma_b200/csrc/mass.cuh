@@ -6,19 +6,19 @@
 namespace ispa {
 
 // log-sum-exp of a query row over both branches; +inf for a row without any key (both -inf), so that
-// exp(s - L) gives every key 0 from it.
+// exp(s - L) gives every key 0 from it.  NaN in either branch stays NaN: fmaxf drops it, the difference does not.
 __device__ __forceinline__ float mass_row_lse(float lse_loc, float lse_hist) {
-  const float hi = fmaxf(lse_loc, lse_hist);
-  if (hi == -INFINITY) return INFINITY;
-  return hi + log1pf(expf(-fabsf(lse_loc - lse_hist)));
+  const float d = lse_loc == lse_hist ? 0.f : fabsf(lse_loc - lse_hist);
+  const float l = fmaxf(lse_loc, lse_hist) + log1pf(expf(-d));
+  return l == -INFINITY ? INFINITY : l;
 }
 
 // The same in 64 bits.  L is one number for all keys of a query, so with few queries its rounding does not
 // average out of the weights: at L = 20 half a unit of fp32 is already 1e-6 of every weight.
 __device__ __forceinline__ double mass_row_lse64(float lse_loc, float lse_hist) {
-  const double hi = fmaxf(lse_loc, lse_hist);
-  if (hi == -INFINITY) return INFINITY;
-  return hi + log1p(exp(-fabs(static_cast<double>(lse_loc) - static_cast<double>(lse_hist))));
+  const double d = lse_loc == lse_hist ? 0.0 : fabs(static_cast<double>(lse_loc) - static_cast<double>(lse_hist));
+  const double l = static_cast<double>(fmaxf(lse_loc, lse_hist)) + log1p(exp(-d));
+  return l == -INFINITY ? INFINITY : l;
 }
 
 // A key's bias is common to all its terms, so it multiplies the sum.  The terms stay finite for the

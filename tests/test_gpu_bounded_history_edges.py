@@ -1,0 +1,39 @@
+"""Bounded-history operators where values are not finite, shares are small or buffers change hands; the
+tolerances are those of test_gpu_bounded_history.py unless a test derives another."""
+import numpy as np
+import pytest
+
+from oracle import ispa_oracle as orc
+from gpu_helpers import ATTN_TOL, host, rel
+from test_gpu_bounded_history import F32_TOL, MASS_TOL, ROW_TOL, check_sparse, dt, lse_of, sparse_case, tensor
+
+pytestmark = pytest.mark.gpu
+
+MASS_CALLS = [("bf16", 128, 2), ("bf16", 64, 20), ("bf16", 128, 200), ("bf16", 64, 300), ("fp32", 32, 5), ("fp32", 128, 40)]
+
+
+def mass_of(q, k, ll, lh, **kw):
+    """The call's weights and the oracle's, [H, n_k]."""
+    import torch
+    from kv_cache_compression_tma_b200 import ispa
+    H, n_k = q.shape[1], k.shape[0]
+    got = ispa.attn_mass(q, k, ll, lh, torch.zeros((H, n_k), device="cuda"), **kw)
+    assert ispa.get_device_status() == ispa.ISPA_OK
+    with np.errstate(all="ignore"):
+        return host(got), orc.attn_mass(host(q), host(k), host(ll), None if lh is None else host(lh), np.zeros((H, n_k)))
+
+
+# ------------------------------------------------------------------------------------------ weights
+@pytest.mark.parametrize("dtype,hd,n_q", MASS_CALLS)
+@pytest.mark.parametrize("hist", ["none", "empty", "finite"])
+def test_mass_keeps_a_nan_log_sum_exp(cuda_ok, dtype, hd, n_q, hist):
+    """A row whose lse_loc is NaN makes every weight of its head NaN, whatever the history's lse is; the other
+    head does not see it."""
+    import torch
+    q, k = tensor((n_q, 2, hd), 1, dt(dtype), 2.0), tensor((150, 2, hd), 2, dt(dtype))
+    ll = lse_of(q, k) + 0.5
+    lh = {"none": None, "empty": torch.full_like(ll, -float("inf")), "finite": ll - 1.0}[hist]
+    ll[0, n_q // 2] = float("nan")
+    got, want = mass_of(q, k, ll, lh)
+    assert np.isnan(want[0]).all() and np.isnan(got[0]).all()
+    assert np.max(np.abs(got[1] - want[1]) / want[1]) <= MASS_TOL
