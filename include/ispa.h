@@ -316,7 +316,8 @@ ISPA_API ispa_status ispa_tempcache_merge(int32_t n_heads, int32_t head_dim, voi
  *   mass_out[h, j] = decay * mass[h, j] + sum_i exp(softmax_scale q_i.k_j + kv_bias[h, j] - L[h, i]),
  *   L[h, i] = log(exp(lse_loc[h, i]) + exp(lse_hist[h, i])),
  * with lse_loc and lse_hist exactly as ispa_dual_stream_attn wrote them for the same queries (fp32
- * [n_heads, n_q], dense; lse_hist NULL = no history branch).  A row with L = -inf adds nothing.
+ * [n_heads, n_q], dense; lse_hist NULL = no history branch).  A row with L = -inf adds nothing,
+ * whatever its scores are; a NaN in lse_loc or lse_hist makes every weight of the head NaN.
  *   q: dtype [n_q, n_heads, head_dim], token stride ld_q; k: dtype [n_k, n_heads, head_dim], token
  *   stride ld_k; mass, mass_out: fp32 [n_heads, >= n_k], row stride ld_mass (both), may be the same
  *   array, else must not overlap; entries from n_k on are left as they are.  decay is finite and >= 0;

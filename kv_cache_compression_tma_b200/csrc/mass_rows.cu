@@ -189,7 +189,8 @@ __global__ void __launch_bounds__(kThreads) mass_rows_kernel(const MassLaunch a)
 #pragma unroll
           for (int e = 0; e < R::kVec; ++e) s = fmaf(qv[e], kv[e], s);
           s = row_sum<R::kLanes>(s);
-          sum[r] += expf((s - li) - li_lo);
+          const float w = expf((s - li) - li_lo);
+          sum[r] += li == INFINITY ? 0.f : w;  // a row without keys adds nothing, whatever its scores are
         }
       }
     }

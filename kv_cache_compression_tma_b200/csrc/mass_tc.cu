@@ -79,7 +79,9 @@ struct Cfg {
   // q_full[kStages], q_empty[kStages], acc_full[kAcc], acc_empty[kAcc], k_full, k_free, k_ready, final
   static constexpr int kNumBars = 2 * kStages + 2 * kAcc + 4;
   static constexpr int kOffMisc = kOffBar + kNumBars * 8 + 8;
-  static constexpr int kSmemBytes = kOffMisc + 16 + 2 * 3 * kTile * 4;  // and the warpgroups' sums of an item, by its parity
+  static constexpr int kOffEmpty = kOffMisc + 16;                // [kChunk / 32] a bit per query: without keys, or past the last
+  static constexpr int kOffSums = kOffEmpty + kChunk / 32 * 4;  // the warpgroups' sums of an item, by its parity
+  static constexpr int kSmemBytes = kOffSums + 2 * 3 * kTile * 4;
   static_assert(kSmemBytes <= 232448, "shared memory budget");
 };
 
@@ -108,7 +110,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::kOffMisc);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::kOffMisc + 4);
   volatile int* never = reinterpret_cast<volatile int*>(smem + C::kOffMisc + 8);
-  float* other = reinterpret_cast<float*>(smem + C::kOffMisc + 16);
+  uint32_t* empty = reinterpret_cast<uint32_t*>(smem + C::kOffEmpty);
+  float* other = reinterpret_cast<float*>(smem + C::kOffSums);
   float* neg_l = reinterpret_cast<float*>(smem + C::kOffL);
 
   const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;  // warp-uniform
@@ -272,6 +275,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int i = tid; i < (c1 - c0 + kQTile - 1) / kQTile * kQTile; i += kEpiThreads) {
             const int64_t o = static_cast<int64_t>(head) * p.n_q + c0 + i;
             neg_l[i] = c0 + i < p.n_q ? -kLog2e * mass_row_lse(p.lse_loc[o], p.lse_hist ? p.lse_hist[o] : -INFINITY) : -INFINITY;
+            const uint32_t bits = __ballot_sync(0xffffffffu, neg_l[i] == -INFINITY);  // the loop's bounds are whole warps
+            if (lane == 0) empty[i / 32] = bits;
           }
           asm volatile("bar.sync 1, %0;" ::"n"(kEpiThreads) : "memory");
           staged_head = head;
@@ -292,11 +297,16 @@ __global__ void __launch_bounds__(kThreads, 1)
             tc_fence_before();  // in registers: free the accumulator for the MMAs before any arithmetic
             __syncwarp();
             if (lane == 0) mbar_arrive(acc_empty + a);
-            const int cols = p.n_q - n * kSub - half * kCols;
-            if (cols < kCols) {  // columns past the last query hold what an earlier product left
+            // Columns past the last query hold what an earlier product left, and the scores of a row without keys
+            // may be anything: 0 there, so that the -inf beside it decides.
 #pragma unroll
-              for (int j = 0; j < kCols; ++j)
-                if (j >= cols) r[j] = 0u;
+            for (int h = 0; h < kCols / 32; ++h) {
+              const uint32_t bits = empty[(n * kSub - c0 + half * kCols) / 32 + h];
+              if (bits != 0) {
+#pragma unroll
+                for (int j = 0; j < 32; ++j)
+                  if ((bits >> j) & 1) r[32 * h + j] = 0u;
+              }
             }
             uint64_t acc[4] = {0ull, 0ull, 0ull, 0ull};
 #pragma unroll

@@ -37,3 +37,17 @@ def test_mass_keeps_a_nan_log_sum_exp(cuda_ok, dtype, hd, n_q, hist):
     got, want = mass_of(q, k, ll, lh)
     assert np.isnan(want[0]).all() and np.isnan(got[0]).all()
     assert np.max(np.abs(got[1] - want[1]) / want[1]) <= MASS_TOL
+
+
+@pytest.mark.parametrize("dtype,hd,n_q", MASS_CALLS)
+@pytest.mark.parametrize("value", [float("nan"), float("inf"), 3e38])
+def test_mass_of_rows_without_keys_whose_scores_are_not_finite(cuda_ok, dtype, hd, n_q, value):
+    """A row whose log-sum-exp is -inf adds nothing, whatever its query holds."""
+    import torch
+    q, k = tensor((n_q, 2, hd), 3, dt(dtype), 2.0), tensor((150, 2, hd), 4, dt(dtype))
+    ll = lse_of(q, k)
+    dead = [0, n_q // 2, n_q - 1] if n_q > 2 else [1]
+    ll[:, dead] = -float("inf")
+    q[dead] = value
+    got, want = mass_of(q, k, ll, torch.full_like(ll, -float("inf")))
+    assert np.max(np.abs(got - want) / want) <= MASS_TOL
