@@ -318,6 +318,9 @@ ISPA_API ispa_status ispa_tempcache_merge(int32_t n_heads, int32_t head_dim, voi
  * with lse_loc and lse_hist exactly as ispa_dual_stream_attn wrote them for the same queries (fp32
  * [n_heads, n_q], dense; lse_hist NULL = no history branch).  A row with L = -inf adds nothing,
  * whatever its scores are; a NaN in lse_loc or lse_hist makes every weight of the head NaN.
+ * The formula also holds for log-sum-exps that leave keys out (those of ispa_block_sparse_attn cover sink,
+ * local and picked keys alone): such a key may weigh more than 1, and its weight is infinite once a term
+ * exp(softmax_scale q_i.k_j - L) passes fp32 (2^127.5 on).
  *   q: dtype [n_q, n_heads, head_dim], token stride ld_q; k: dtype [n_k, n_heads, head_dim], token
  *   stride ld_k; mass, mass_out: fp32 [n_heads, >= n_k], row stride ld_mass (both), may be the same
  *   array, else must not overlap; entries from n_k on are left as they are.  decay is finite and >= 0;

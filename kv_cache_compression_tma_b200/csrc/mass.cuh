@@ -22,7 +22,7 @@ __device__ __forceinline__ double mass_row_lse64(float lse_loc, float lse_hist) 
 }
 
 // A key's bias is common to all its terms, so it multiplies the sum.  The terms stay finite for the
-// biases the attention admits: L covers the key itself, so s - L <= -b <= 64.  An excluded key (bias
+// biases the attention admits where L covers the key itself, so that s - L <= -b <= 64.  An excluded key (bias
 // -inf, or so low that its factor is 0) is in no row's L, and its sum may be anything: it gets 0
 // whatever the sum is.
 __device__ __forceinline__ float mass_apply_bias(float sum, float bias) {

@@ -49,8 +49,8 @@ constexpr int kFirstEpiWarp = 3;
 constexpr int kEpiThreads = 512;
 constexpr int kThreads = 32 * kFirstEpiWarp + kEpiThreads;
 // Of eight pairs of queries, those whose exponentials run on the multiply-add pipes, the others on the
-// special-function unit: it alone takes 16 a clock, less than the products deliver.  (No exponent passes
-// 127: a key that counts has no weight above exp(-bias) <= e^64.)
+// special-function unit: it alone takes 16 a clock, less than the products deliver.  They have sums of their own,
+// which are infinite once one of them passes 2^127.5 (the polynomial's end; clamping each at 128 instead cost 3 %).
 constexpr int kPolyPairs = 0b10001000;
 constexpr float kLog2e = 1.4426950408889634f;
 
@@ -308,7 +308,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                   if ((bits >> j) & 1) r[32 * h + j] = 0u;
               }
             }
-            uint64_t acc[4] = {0ull, 0ull, 0ull, 0ull};
+            uint64_t acc[4] = {0ull, 0ull, 0ull, 0ull};  // [3]: the polynomials'
+            float most = -INFINITY;                      // their largest exponent
 #pragma unroll
             for (int j = 0; j < kCols; j += 4) {
               const float4 l4 = *reinterpret_cast<const float4*>(nl + j);
@@ -317,13 +318,15 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const int pair = j >> 1 | h;
                 const uint64_t y = fma_f2(pack_f2(__uint_as_float(r[j + 2 * h]), __uint_as_float(r[j + 2 * h + 1])), sl2x2,
                                           h ? pack_f2(l4.z, l4.w) : pack_f2(l4.x, l4.y));
+                float y0, y1;
+                unpack_f2(y, y0, y1);
                 if ((kPolyPairs >> (pair & 7)) & 1) {
                   uint64_t pv, scale;
                   exp2_poly2(y, pv, scale);
-                  acc[pair & 3] = fma_f2(pv, scale, acc[pair & 3]);
+                  acc[3] = fma_f2(pv, scale, acc[3]);
+                  most = max3f_nan(most, y0, y1);
                 } else {
-                  float y0, y1;
-                  unpack_f2(y, y0, y1);
+                  static_assert((kPolyPairs & 0x77) == 0, "the fourth sum is the polynomials'");
                   acc[pair & 3] = add_f2(acc[pair & 3], pack_f2(fast_exp2(y0), fast_exp2(y1)));
                 }
               }
@@ -333,6 +336,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             unpack_f2(acc[1], a2, a3);
             unpack_f2(acc[2], a4, a5);
             unpack_f2(acc[3], a6, a7);
+            if (most > 127.5f) a6 = a7 = INFINITY;
             total += ((a0 + a1) + (a2 + a3)) + ((a4 + a5) + (a6 + a7));
           }
         }

@@ -302,6 +302,13 @@ __device__ __forceinline__ float max3f(float a, float b, float c) {
   return d;
 }
 
+// The same, NaN if any of the three is.
+__device__ __forceinline__ float max3f_nan(float a, float b, float c) {
+  float d;
+  asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
+
 // Packed pairs of fp32 in one 64-bit register for the sm_100 f32x2 FMA / add instructions.
 __device__ __forceinline__ uint64_t pack_f2(float lo, float hi) {
   uint64_t r;
@@ -332,7 +339,7 @@ __device__ __forceinline__ float fast_exp2(float x) {
 // [-1/2, 1/2] (weighted least squares iterated to equal ripple: largest relative error 2.7e-6, mean
 // 4e-8, so a sum of many loses nothing), and 2^n from n's bits.  Returns the polynomial's value and
 // 2^n apart: the caller's accumulation multiplies them.  y below -127 gives n = -127, whose 2^n is 0;
-// NaN stays NaN; y must stay below 127.
+// NaN stays NaN; above 127.5 the result is anything, and the caller has to look for that.
 __device__ __forceinline__ void exp2_poly2(uint64_t y, uint64_t& p, uint64_t& scale) {
   float y0, y1;
   unpack_f2(y, y0, y1);

@@ -468,7 +468,8 @@ def attn_mass(q, k, lse_loc, lse_hist, mass, *, kv_bias=None, decay: float = 1.0
               cuda_cores: bool = False, mass_out=None, stream=None):
     """ispa_attn_mass: mass[h, j] = decay * mass[h, j] + the attention weight that key j collects from the
     queries q [n_q, H, hd], for the keys k [n_k, H, hd] of one segment.  lse_loc, lse_hist: fp32 [H, n_q],
-    contiguous, as dual_stream_attn returned them for the same queries (lse_hist None: no history branch).
+    contiguous, as dual_stream_attn returned them for the same queries (lse_hist None: no history branch);
+    those of block_sparse_attn leave out the keys that were not picked, which may then weigh more than 1.
     kv_bias: fp32 [H, >= n_k], the segment's bias in that call.  mass fp32 [H, >= n_k]; the result goes to
     mass_out (same shape and stride as mass) or back into mass.  Returns the array written."""
     import torch
@@ -552,7 +553,8 @@ class MassCache:
         return self.k[:self.n], self.v[:self.n]
 
     def accumulate(self, q, lse_loc, lse_hist=None, *, decay: float = 1.0, softmax_scale: float = 0.0, stream=None):
-        """Add the weights that the held keys collected from q in the attention call that gave the lse's."""
+        """Add the weights that the held keys collected from q in the attention call that gave the lse's (over all
+        held keys: see attn_mass for lse's that leave some out)."""
         attn_mass(q, self.k[:self.n], lse_loc, lse_hist, self.mass, decay=decay, softmax_scale=softmax_scale,
                   stream=stream)
 

@@ -51,3 +51,22 @@ def test_mass_of_rows_without_keys_whose_scores_are_not_finite(cuda_ok, dtype, h
     q[dead] = value
     got, want = mass_of(q, k, ll, torch.full_like(ll, -float("inf")))
     assert np.max(np.abs(got - want) / want) <= MASS_TOL
+
+
+@pytest.mark.parametrize("n_q", [8, 200])
+def test_mass_of_weights_past_the_largest_number(cuda_ok, n_q):
+    """Log-sum-exps that do not cover the key (those of attention over selected blocks, say): a weight may
+    pass 1, and past fp32 it is infinite, whichever query it comes from.  Weights up to e^80 stay exact:
+    |logit| + |L| <= 100 in the exponent is 100 2^-24 = 6e-6 of MASS_TOL."""
+    import torch
+    q, k = tensor((n_q, 1, 128), 5, torch.bfloat16, 2.0), tensor((150, 1, 128), 6, torch.bfloat16)
+    bias = torch.zeros((1, 150), device="cuda")
+    bias[:, 3] = -float("inf")
+    for i in range(8):
+        ll = torch.full((1, n_q), 9.0, device="cuda")
+        ll[:, i] = -200.0
+        got, _ = mass_of(q, k, ll, None, kv_bias=bias)
+        assert got[0, 3] == 0 and np.isposinf(np.delete(got[0], 3)).all(), i
+        ll[:, i] = -65.0
+        got, want = mass_of(q, k, ll, None)
+        assert np.max(np.abs(got - want) / want) <= MASS_TOL, i
