@@ -52,6 +52,10 @@ struct Kind {
 __device__ __forceinline__ void cp_async16(uint32_t smem_dst, const void* src) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_dst), "l"(src) : "memory");
 }
+// The same, zeros where `real` is false (src is not read then).
+__device__ __forceinline__ void cp_async16_or_zero(uint32_t smem_dst, const void* src, bool real) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_dst), "l"(src), "r"(real ? 16 : 0) : "memory");
+}
 
 template <typename T, int HD, bool kAligned>
 __global__ void __launch_bounds__(Kind<T, HD, kAligned>::kThreads, Kind<T, HD, kAligned>::kCtas)
@@ -139,7 +143,7 @@ __global__ void __launch_bounds__(Kind<T, HD, kAligned>::kThreads, Kind<T, HD, k
   constexpr int kPK = HD / 32;  // pieces of a lane per key row
   constexpr int kChunks = HD / 8;
   auto stage_of = [&](int st) { return ring + (warp * kStages + st) * X::kPieces * 32; };
-  auto fetch = [&](int st, int seg, int key0, int n) {  // rows past the end repeat the last key
+  auto fetch = [&](int st, int seg, int key0, int n) {  // past the end: the last key again, values of 0
     const int64_t ld_k = a.ld_k[seg], ld_v = a.ld_v[seg];
     const T* k_lo = static_cast<const T*>(a.k[seg]) + static_cast<int64_t>(head) * HD + 8 * mc + (key0 + min(mg, n - 1)) * ld_k;
     const T* k_hi = k_lo + (min(mg + 8, n - 1) - min(mg, n - 1)) * ld_k;
@@ -153,8 +157,9 @@ __global__ void __launch_bounds__(Kind<T, HD, kAligned>::kThreads, Kind<T, HD, k
 #pragma unroll
     for (int i = 0; i < 16 / R::kPerWarp; ++i) {
       const int r = i * R::kPerWarp + grp;
-      cp_async16(dst + (2 * kPK * 32 + r * kChunks + (gl ^ (r & 7))) * 16, V);
-      if (r + R::kPerWarp < n) V += R::kPerWarp * ld_v;  // else the last row read repeats
+      // a weight of 0 times the last value again would be NaN where that is infinite
+      cp_async16_or_zero(dst + (2 * kPK * 32 + r * kChunks + (gl ^ (r & 7))) * 16, V, r < n);
+      if (r + R::kPerWarp < n) V += R::kPerWarp * ld_v;  // else V stays in bounds
     }
   };
   auto work_mma = [&](int st, int n, float& mb, float& lb, float (*ab)[4]) {

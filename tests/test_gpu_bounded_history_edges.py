@@ -70,3 +70,30 @@ def test_mass_of_weights_past_the_largest_number(cuda_ok, n_q):
         ll[:, i] = -65.0
         got, want = mass_of(q, k, ll, None)
         assert np.max(np.abs(got - want) / want) <= MASS_TOL, i
+
+
+# ------------------------------------------------------------------------------------------ sparse attention
+@pytest.mark.parametrize("dtype,hd,n_q,q_block", [("bf16", 64, 2, 1), ("bf16", 128, 2, 1), ("bf16", 128, 3, 128), ("bf16", 64, 200, 128),
+                                                  ("bf16", 128, 200, 128), ("fp32", 64, 3, 2)])
+@pytest.mark.parametrize("last", [1, 2, 4, 9])
+def test_sparse_infinite_values_stay_infinite(cuda_ok, dtype, hd, n_q, q_block, last):
+    """An infinity in the `last`-th value row from the end of the local keys (5, 16 + 13 of them) or of the
+    history gives that infinity in its column, wherever the key lies in its tile."""
+    import torch
+    from kv_cache_compression_tma_b200 import ispa
+    for n_loc in (5, 29):
+        if last > n_loc:
+            continue
+        t, _ = sparse_case(dtype, 2, hd, n_q, q_block, 0, n_loc, 75, 64, 2, 80)
+        idx = torch.tensor([0, 1], dtype=torch.int32, device="cuda").repeat(2, -(-n_q // q_block), 1)
+        t["v_loc"][-last, :, 3] = float("inf")
+        t["v_hist"][-last, :, 7] = -float("inf")
+        out = ispa.block_sparse_attn(*t.values(), idx, block=64, q_block=q_block)
+        with np.errstate(all="ignore"):
+            ref = orc.block_sparse(*(host(x) for x in t.values()), idx.cpu().numpy(), 64, q_block)
+        tol = F32_TOL if dtype == "fp32" else ROW_TOL if n_q < 100 else ATTN_TOL
+        for got, want, w in ((out["o_loc"], ref["O_loc"], "o_loc"), (out["o_full"], ref["O_full"], "o_full")):
+            got, want = host(got).reshape(want.shape), want
+            inf = np.isinf(want)
+            assert inf[..., 3].all() and inf[..., 7].any() == (w == "o_full")
+            assert np.array_equal(got[inf], want[inf]) and rel(got[~inf], want[~inf]) <= tol[w], (w, n_loc)
