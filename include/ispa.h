@@ -394,7 +394,8 @@ ISPA_API ispa_status ispa_block_select(int32_t dtype, int32_t n_heads, int32_t h
 /*
  * ispa_block_sparse_attn: ispa_dual_stream_attn with the history branch over the listed blocks only.
  * args: as there (five outputs, the same layouts); kv_bias must be NULL in every segment (else
- * ISPA_ERR_UNSUPPORTED).  n_kv[ISPA_SEG_HIST] is the whole history's length.
+ * ISPA_ERR_UNSUPPORTED).  n_kv[ISPA_SEG_HIST] is the whole history's length.  D is formed as
+ * sigma(lse_hist - lse_loc) (O_hist - O_loc), so a history of small weight keeps its relative accuracy.
  *   idx: int32 [n_heads, ceil(n_q / q_block), n_sel], dense (device): the blocks of query group i are
  *   idx[h, i, :], in any order; an entry outside 0 .. ceil(n_hist / block) - 1 names no block, a block
  *   listed twice counts twice.  A row without any history key gets lse_hist = -inf, O_full = O_loc and

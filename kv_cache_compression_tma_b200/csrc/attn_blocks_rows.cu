@@ -388,11 +388,12 @@ __global__ void __launch_bounds__(Kind<T, HD, kAligned>::kThreads, Kind<T, HD, k
     const float lse_l = mx[0] + log2f(sum[0]);
     const float lse_h = has_hist ? mx[1] + log2f(sum[1]) : -INFINITY;
     const float vl = o[0] / sum[0];
-    float vf = vl;
+    float vf = vl, vd = vl - vl;
     if (has_hist) {
       const float top = fmaxf(lse_l, lse_h);
-      const float wl = exp2f(lse_l - top), wh = exp2f(lse_h - top);
-      vf = (wl * vl + wh * (o[1] / sum[1])) / (wl + wh);
+      const float wl = exp2f(lse_l - top), wh = exp2f(lse_h - top), vh = o[1] / sum[1];
+      vf = (wl * vl + wh * vh) / (wl + wh);
+      vd = wh / (wl + wh) * (vh - vl);  // vf - vl would lose a share below the rounding of vf
     }
     const int64_t at = row * a.ld_o + static_cast<int64_t>(head) * HD + tid;
     auto put = [&](void* base, float v) {
@@ -403,7 +404,7 @@ __global__ void __launch_bounds__(Kind<T, HD, kAligned>::kThreads, Kind<T, HD, k
     };
     put(a.o_loc, vl);
     put(a.o_full, vf);
-    if (a.d_out) put(a.d_out, vf - vl);
+    if (a.d_out) put(a.d_out, vd);
     if (tid == 0) {
       a.lse_loc[static_cast<int64_t>(head) * a.n_q + row] = lse_l * ln2;
       a.lse_hist[static_cast<int64_t>(head) * a.n_q + row] = has_hist ? lse_h * ln2 : -INFINITY;

@@ -3,7 +3,7 @@
 //
 // Keys are walked once in tiles of 128, local branch first, with an online softmax (m, l, fp32
 // accumulator in TMEM) per branch, and
-//   O_loc = O_A / l_loc,  O_full = w_loc O_loc + w_hist O_B / l_hist,  D = O_full - O_loc.
+//   O_loc = O_A / l_loc,  O_full = w_loc O_loc + w_hist O_B / l_hist,  D = w_hist (O_B / l_hist - O_loc).
 // The CTA first turns its list into halves of 64 keys (a block is one or two of them; entries that name
 // no block, and empty halves of the history's last block, are dropped), and a history tile is any two
 // consecutive halves: two 64-row TMA boxes per 64 columns instead of one 128-row box.  So both block
@@ -499,7 +499,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_blocks_tc_kernel(const __gri
             for (int j = 0; j < 8; ++j) {
               vl[j] += lo[j];
               vf[j] = fmaf(w_loc, vl[j], w_hist * o[8 * i + j]);
-              vd[j] = vf[j] - vl[j];
+              vd[j] = w_hist * (o[8 * i + j] - vl[j]);  // vf - vl would lose a share below the rounding of vf
             }
           } else {
 #pragma unroll

@@ -97,3 +97,25 @@ def test_sparse_infinite_values_stay_infinite(cuda_ok, dtype, hd, n_q, q_block, 
             inf = np.isinf(want)
             assert inf[..., 3].all() and inf[..., 7].any() == (w == "o_full")
             assert np.array_equal(got[inf], want[inf]) and rel(got[~inf], want[~inf]) <= tol[w], (w, n_loc)
+
+
+def small_share(dtype, H, hd, n_q, q_block, n_loc, seed, scale=1.0):
+    """A case whose history weighs next to nothing: queries of positive elements (about 2.6 each) against history
+    keys moved by -0.8, so that the scores lie 2.6 * 0.8 * sqrt(hd) lower."""
+    import torch
+    t, _ = sparse_case(dtype, H, hd, n_q, q_block, 6, n_loc, 200, 64, 3, seed)
+    t["q"].copy_(t["q"].abs() + 1)
+    t["k_hist"].sub_(0.8)
+    for name in ("v_sink", "v_loc"):
+        t[name].mul_(scale)
+    return t, torch.tensor([0, 1, 3], dtype=torch.int32, device="cuda").repeat(H, -(-n_q // q_block), 1)
+
+
+@pytest.mark.parametrize("dtype,hd,n_q,q_block", [("fp32", 64, 3, 1), ("fp32", 128, 5, 4), ("bf16", 64, 2, 1), ("bf16", 128, 3, 128),
+                                                  ("bf16", 64, 200, 128), ("bf16", 128, 200, 128)])
+def test_sparse_difference_of_a_small_share(cuda_ok, dtype, hd, n_q, q_block):
+    """D = O_full - O_loc keeps its relative accuracy where the history's share (here about 1e-7 and less) is
+    below the rounding of O_full."""
+    t, idx = small_share(dtype, 2, hd, n_q, q_block, 90, 81)
+    out = check_sparse(t, idx, 64, q_block, F32_TOL if dtype == "fp32" else ROW_TOL if n_q < 100 else ATTN_TOL)
+    assert np.abs(host(out["d"])).max() < 1e-4
