@@ -13,8 +13,10 @@
 // its maximum or waits while the other keeps the exponentials going.  Both scale by one running maximum per
 // row, which a group reads after the other's last tile and hands on (m_ready); each keeps a partial
 // sum of its own.  S runs two tiles ahead of P V in three TMEM buffers.  That leaves one accumulator: at
-// the branch switch O_loc goes to its place in memory, rounded, and what the rounding left goes to
-// O_full's place, where the same thread finds it again for the epilogue (together 16 bits of O_loc).
+// the branch switch O_loc goes to its place in memory, rounded, and the bits that the rounding took go to
+// O_full's place, where the same thread finds them again for the epilogue (together the 32 bits of O_loc).
+// P is rounded to bf16 for its product, as in the dense kernel: the tensor cores take no wider operand
+// beside bf16 values, and a second product for what the rounding left would cost half as much again.
 //
 // Bound: the loop of three tiles (softmax of one, P V and the S that waits for its buffer) at about 1430
 // clocks per tile (1024 of MMA), and power.  12 heads x 4680 queries over 6240 local keys and 64 blocks of
@@ -322,7 +324,10 @@ __global__ void __launch_bounds__(kThreads, 1) attn_blocks_tc_kernel(const __gri
     auto pack8 = [](const float* v) {
       return make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7]));
     };
-    // O_loc rounded goes to its place; with a history, what the rounding left waits in O_full's place
+    // O_loc rounded goes to its place; with a history, the lower 16 bits of the fp32 value wait in O_full's.  Read as
+    // a signed number they are what the rounding left, so adding them below the rounded value's bits gives the
+    // fp32 value again; only a value halfway between two bf16 ones (read as -32768 either way) cannot be told
+    // from its neighbour and moves to the even one's side first, by one unit of fp32.
     auto store_local = [&]() {
       const float inv_l = 1.f / l_row;
 #pragma unroll 1
@@ -332,16 +337,35 @@ __global__ void __launch_bounds__(kThreads, 1) attn_blocks_tc_kernel(const __gri
         if (!live_row) continue;
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-          const uint4 hi = pack8(o + 8 * i);
-          *reinterpret_cast<uint4*>(p.o_loc + o_at + c * 16 + 8 * i) = hi;
           if (has_hist) {
-            float h[8], lo[8];
-            unpack<__nv_bfloat16>(hi, h);
+            uint32_t lo[4];
 #pragma unroll
-            for (int j = 0; j < 8; ++j) lo[j] = isinf(h[j]) ? 0.f : o[8 * i + j] - h[j];
-            *reinterpret_cast<uint4*>(p.o_full + o_at + c * 16 + 8 * i) = pack8(lo);
+            for (int j = 0; j < 8; j += 2) {
+              uint32_t b[2];
+#pragma unroll
+              for (int x = 0; x < 2; ++x) {
+                b[x] = __float_as_uint(o[8 * i + j + x]);
+                if ((b[x] & 0xFFFFu) == 0x8000u) b[x] += (b[x] & 0x10000u) ? 1u : 0xFFFFFFFFu;
+                o[8 * i + j + x] = __uint_as_float(b[x]);
+              }
+              lo[j / 2] = __byte_perm(b[0], b[1], 0x5410);
+            }
+            *reinterpret_cast<uint4*>(p.o_full + o_at + c * 16 + 8 * i) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
           }
+          *reinterpret_cast<uint4*>(p.o_loc + o_at + c * 16 + 8 * i) = pack8(o + 8 * i);
         }
+      }
+    };
+    // the eight values of O_loc set aside at `at`
+    auto load_local = [&](int64_t at, float* v) {
+      const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
+      const uint4 hi4 = live_row ? *reinterpret_cast<const uint4*>(p.o_loc + at) : zero;
+      const uint4 lo4 = live_row ? *reinterpret_cast<const uint4*>(p.o_full + at) : zero;
+      const uint32_t hi[4] = {hi4.x, hi4.y, hi4.z, hi4.w}, lo[4] = {lo4.x, lo4.y, lo4.z, lo4.w};
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        v[2 * j] = __uint_as_float((hi[j] << 16) + static_cast<uint32_t>(static_cast<int32_t>(lo[j] << 16) >> 16));
+        v[2 * j + 1] = __uint_as_float((hi[j] & 0xFFFF0000u) + static_cast<uint32_t>(static_cast<int32_t>(lo[j]) >> 16));
       }
     };
 
@@ -490,14 +514,10 @@ __global__ void __launch_bounds__(kThreads, 1) attn_blocks_tc_kernel(const __gri
         for (int i = 0; i < 2; ++i) {
           float vf[8], vd[8];
           if (has_hist) {
-            float vl[8], lo[8];
-            const int64_t at = o_at + c * 16 + 8 * i;
-            const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
-            unpack<__nv_bfloat16>(live_row ? *reinterpret_cast<const uint4*>(p.o_loc + at) : zero, vl);
-            unpack<__nv_bfloat16>(live_row ? *reinterpret_cast<const uint4*>(p.o_full + at) : zero, lo);
+            float vl[8];
+            load_local(o_at + c * 16 + 8 * i, vl);
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
-              vl[j] += lo[j];
               vf[j] = fmaf(w_loc, vl[j], w_hist * o[8 * i + j]);
               vd[j] = w_hist * (o[8 * i + j] - vl[j]);  // vf - vl would lose a share below the rounding of vf
             }

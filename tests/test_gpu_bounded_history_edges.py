@@ -119,3 +119,20 @@ def test_sparse_difference_of_a_small_share(cuda_ok, dtype, hd, n_q, q_block):
     t, idx = small_share(dtype, 2, hd, n_q, q_block, 90, 81)
     out = check_sparse(t, idx, 64, q_block, F32_TOL if dtype == "fp32" else ROW_TOL if n_q < 100 else ATTN_TOL)
     assert np.abs(host(out["d"])).max() < 1e-4
+
+
+@pytest.mark.parametrize("hd", [64, 128])
+@pytest.mark.parametrize("scale", [1.0, 2.0 ** -128])
+def test_sparse_local_output_is_held_in_32_bits(cuda_ok, hd, scale):
+    """Under a history that weighs nothing O_full is O_loc: the local output that the tensor-core kernel sets
+    aside while it walks the history comes back as it was, so both round alike (subnormal ones too)."""
+    import torch
+    from kv_cache_compression_tma_b200 import ispa
+    t, idx = small_share("bf16", 2, hd, 700, 128, 300, 82, scale)
+    for name in ("v_hist",):
+        t[name].mul_(scale)
+    t["k_hist"].sub_(3.0)
+    out = ispa.block_sparse_attn(*t.values(), idx, block=64, q_block=128)
+    assert ispa.get_device_status() == ispa.ISPA_OK
+    assert torch.isfinite(out["o_full"]).all() and torch.isfinite(out["lse_hist"]).all()
+    assert torch.equal(out["o_full"], out["o_loc"])
