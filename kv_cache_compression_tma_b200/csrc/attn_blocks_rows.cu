@@ -11,7 +11,7 @@
 //   bf16 and what the rounding left (so p keeps 16 bits, at no further instruction).  Each warp copies
 //   its units ahead (cp.async) into its own ring of kStages units in shared memory.  (By multiply-adds
 //   and shuffles a unit took over 400 instructions, and their latency, not memory, set the pace.)
-//   Other cases: a key row spans kLanes lanes (16 bytes each), units of 8 warp-wide loads, dot products
+//   Other cases (and bf16 with ISPA_ATTN_CUDA_CORES): a key row spans kLanes lanes (16 bytes each), units of 8 warp-wide loads, dot products
 //   by multiply-adds and shuffles, a state per lane group.
 // Bound: the read of the keys and values, each once.
 #include <cooperative_groups.h>
@@ -38,9 +38,11 @@ struct State {  // one branch's state of a CTA
   float acc[HD];
 };
 
-template <typename T, int HD, bool kAligned>
+// kMma: both products by mma.sync (bf16, head_dim 64 or 128, aligned rows), else by multiply-adds.
+template <typename T, int HD, bool kAligned, bool kMma_>
 struct Kind {
-  static constexpr bool kMma = sizeof(T) == 2 && kAligned && HD >= 64;
+  static constexpr bool kMma = kMma_;
+  static_assert(!kMma || (sizeof(T) == 2 && kAligned && HD >= 64), "fragments of aligned bf16 rows");
   static constexpr int kUnit = kMma ? 16 : kLoads * Row<T, HD>::kPerWarp;  // keys per unit
   static constexpr int kWarps = 8;
   static constexpr int kThreads = 32 * kWarps;
@@ -57,12 +59,11 @@ __device__ __forceinline__ void cp_async16_or_zero(uint32_t smem_dst, const void
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_dst), "l"(src), "r"(real ? 16 : 0) : "memory");
 }
 
-template <typename T, int HD, bool kAligned>
-__global__ void __launch_bounds__(Kind<T, HD, kAligned>::kThreads, Kind<T, HD, kAligned>::kCtas)
+template <typename T, int HD, bool kAligned, bool kMma>
+__global__ void __launch_bounds__(Kind<T, HD, kAligned, kMma>::kThreads, Kind<T, HD, kAligned, kMma>::kCtas)
     attn_blocks_rows_kernel(const AttnLaunch a, const BlockList b) {
   using R = Row<T, HD>;
-  using X = Kind<T, HD, kAligned>;
-  constexpr bool kMma = X::kMma;
+  using X = Kind<T, HD, kAligned, kMma>;
   constexpr int kUnit = X::kUnit, kWarps = X::kWarps, kThreads = X::kThreads;
   extern __shared__ __align__(16) uint4 ring[];  // [warp][stage][piece][lane]
   __shared__ float sm[2][kWarps], sl[2][kWarps];
@@ -412,14 +413,14 @@ __global__ void __launch_bounds__(Kind<T, HD, kAligned>::kThreads, Kind<T, HD, k
   }
 }
 
-template <typename T, int HD, bool kAligned>
+template <typename T, int HD, bool kAligned, bool kMma>
 cudaError_t launch_kind(const AttnLaunch& a, const BlockList& b, cudaStream_t s, int* n) {
-  using X = Kind<T, HD, kAligned>;
+  using X = Kind<T, HD, kAligned, kMma>;
   // Cluster size: split a row's keys while all CTAs still run at once and a warp keeps at least two units.
   const int64_t keys = a.n_kv[0] + a.n_kv[1] + static_cast<int64_t>(b.n_sel) * b.block;
   const int64_t most = std::min(X::kCtas * 148 / (a.n_q * a.n_heads), keys / (static_cast<int64_t>(2) * X::kWarps * X::kUnit));
   const int C = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(kMaxCluster, most)));
-  auto kernel = attn_blocks_rows_kernel<T, HD, kAligned>;
+  auto kernel = attn_blocks_rows_kernel<T, HD, kAligned, kMma>;
   if (X::kSmem > 0) {
     const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, X::kSmem);
     if (e != cudaSuccess) return e;
@@ -442,33 +443,36 @@ cudaError_t launch_kind(const AttnLaunch& a, const BlockList& b, cudaStream_t s,
 }
 
 template <typename T, int HD>
-cudaError_t launch_hd(const AttnLaunch& a, const BlockList& b, cudaStream_t s, int* n) {
+cudaError_t launch_hd(const AttnLaunch& a, const BlockList& b, bool cuda_cores, cudaStream_t s, int* n) {
   bool al = true;
   for (int i = 0; i < 3; ++i)
     if (a.n_kv[i] > 0)
       al = al && aligned16(a.k[i]) && aligned16(a.v[i]) && a.ld_k[i] * static_cast<int64_t>(sizeof(T)) % 16 == 0 &&
            a.ld_v[i] * static_cast<int64_t>(sizeof(T)) % 16 == 0;
-  return al ? launch_kind<T, HD, true>(a, b, s, n) : launch_kind<T, HD, false>(a, b, s, n);
+  if constexpr (sizeof(T) == 2 && HD >= 64) {
+    if (al && !cuda_cores) return launch_kind<T, HD, true, true>(a, b, s, n);
+  }
+  return al ? launch_kind<T, HD, true, false>(a, b, s, n) : launch_kind<T, HD, false, false>(a, b, s, n);
 }
 
 template <typename T>
-cudaError_t launch_t(const AttnLaunch& a, const BlockList& b, cudaStream_t s, int* n) {
+cudaError_t launch_t(const AttnLaunch& a, const BlockList& b, bool cuda_cores, cudaStream_t s, int* n) {
   switch (a.head_dim) {
     case 16:
-      return launch_hd<T, 16>(a, b, s, n);
+      return launch_hd<T, 16>(a, b, cuda_cores, s, n);
     case 32:
-      return launch_hd<T, 32>(a, b, s, n);
+      return launch_hd<T, 32>(a, b, cuda_cores, s, n);
     case 64:
-      return launch_hd<T, 64>(a, b, s, n);
+      return launch_hd<T, 64>(a, b, cuda_cores, s, n);
     default:
-      return launch_hd<T, 128>(a, b, s, n);
+      return launch_hd<T, 128>(a, b, cuda_cores, s, n);
   }
 }
 
 }  // namespace
 
-cudaError_t launch_attn_blocks_rows(const AttnLaunch& a, const BlockList& b, cudaStream_t s, int* n_launched) {
-  return a.dtype == 1 ? launch_t<float>(a, b, s, n_launched) : launch_t<__nv_bfloat16>(a, b, s, n_launched);
+cudaError_t launch_attn_blocks_rows(const AttnLaunch& a, const BlockList& b, bool cuda_cores, cudaStream_t s, int* n_launched) {
+  return a.dtype == 1 ? launch_t<float>(a, b, cuda_cores, s, n_launched) : launch_t<__nv_bfloat16>(a, b, cuda_cores, s, n_launched);
 }
 
 }  // namespace ispa

@@ -180,8 +180,9 @@ struct BlockList {
 // tcgen05 kernel: bf16, attn_tc_supported's rules, block 64 or 128, q_block a multiple of 128
 bool attn_blocks_tc_supported(const AttnLaunch& a, const BlockList& b);
 cudaError_t launch_attn_blocks_tc(const AttnLaunch& a, const BlockList& b, cudaStream_t s, int* n_launched);
-// one row and head per cluster, CUDA cores (either dtype, any head_dim of the API, any alignment)
-cudaError_t launch_attn_blocks_rows(const AttnLaunch& a, const BlockList& b, cudaStream_t s, int* n_launched);
+// one row and head per cluster (either dtype, any head_dim of the API, any alignment); cuda_cores: fp32
+// multiply-adds also where bf16 rows could go through mma.sync
+cudaError_t launch_attn_blocks_rows(const AttnLaunch& a, const BlockList& b, bool cuda_cores, cudaStream_t s, int* n_launched);
 
 struct BlockMeansLaunch {
   int dtype;
@@ -232,8 +233,9 @@ struct MassLaunch {
 bool mass_tc_supported(const MassLaunch& a);
 cudaError_t launch_mass_tc(const MassLaunch& a, cudaStream_t s, int* n_launched);
 // any case; bf16 calls of up to kMassFewQueries queries over aligned keys read them at the memory's rate
+// (mma.sync), unless cuda_cores asks for fp32 multiply-adds
 constexpr int64_t kMassFewQueries = 32;
-cudaError_t launch_mass_rows(const MassLaunch& a, cudaStream_t s, int* n_launched);
+cudaError_t launch_mass_rows(const MassLaunch& a, bool cuda_cores, cudaStream_t s, int* n_launched);
 
 // ------------------------------------------------------------------ cache insertion with eviction
 struct InsertLaunch {

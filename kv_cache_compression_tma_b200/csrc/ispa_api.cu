@@ -446,7 +446,7 @@ ispa_status ispa_attn_mass(int32_t dtype, int32_t n_heads, int32_t head_dim, con
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   int n = 0;
   const bool tc = !cuda_cores && n_q > kMassFewQueries && mass_tc_supported(L);
-  cudaError_t e = tc ? launch_mass_tc(L, st, &n) : launch_mass_rows(L, st, &n);
+  cudaError_t e = tc ? launch_mass_tc(L, st, &n) : launch_mass_rows(L, cuda_cores, st, &n);
   count(n);
   return e == cudaSuccess ? ISPA_OK : ISPA_ERR_CUDA;
 }
@@ -547,7 +547,7 @@ ispa_status ispa_block_sparse_attn(const ispa_attn_args* a, const int32_t* idx, 
   if (!L.status) return ISPA_ERR_CUDA;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   int n = 0;
-  cudaError_t e = rows ? launch_attn_blocks_rows(L, B, st, &n) : launch_attn_blocks_tc(L, B, st, &n);
+  cudaError_t e = rows ? launch_attn_blocks_rows(L, B, cuda_cores, st, &n) : launch_attn_blocks_tc(L, B, st, &n);
   count(n);
   return e == cudaSuccess ? ISPA_OK : ISPA_ERR_CUDA;
 }

@@ -257,8 +257,8 @@ cudaError_t launch_t(const MassLaunch& a, cudaStream_t s, int* n) {
 
 }  // namespace
 
-cudaError_t launch_mass_rows(const MassLaunch& a, cudaStream_t s, int* n_launched) {
-  if (a.dtype == 0 && a.n_q >= 1 && a.n_q <= kMassFewQueries && (a.head_dim == 64 || a.head_dim == 128) && aligned16(a.k) && a.ld_k % 8 == 0)
+cudaError_t launch_mass_rows(const MassLaunch& a, bool cuda_cores, cudaStream_t s, int* n_launched) {
+  if (!cuda_cores && a.dtype == 0 && a.n_q >= 1 && a.n_q <= kMassFewQueries && (a.head_dim == 64 || a.head_dim == 128) && aligned16(a.k) && a.ld_k % 8 == 0)
     return a.head_dim == 128 ? launch_few<128>(a, s, n_launched) : launch_few<64>(a, s, n_launched);
   return a.dtype == 1 ? launch_t<float>(a, s, n_launched) : launch_t<__nv_bfloat16>(a, s, n_launched);
 }

@@ -136,3 +136,21 @@ def test_sparse_local_output_is_held_in_32_bits(cuda_ok, hd, scale):
     assert ispa.get_device_status() == ispa.ISPA_OK
     assert torch.isfinite(out["o_full"]).all() and torch.isfinite(out["lse_hist"]).all()
     assert torch.equal(out["o_full"], out["o_loc"])
+
+
+# ------------------------------------------------------------------------------------------ the flag
+def test_cuda_cores_flag_asks_for_fp32_arithmetic(cuda_ok):
+    """With cuda_cores the same values give the same bits at any alignment: aligned rows take the multiply-add
+    form too."""
+    import torch
+    from kv_cache_compression_tma_b200 import ispa
+    for hd, n_q in ((64, 3), (128, 20), (128, 40)):
+        qk = [(tensor((n_q, 2, hd), 7, torch.bfloat16, 2.0, p, p), tensor((150, 2, hd), 8, torch.bfloat16, 1.0, p, p)) for p in (0, 1)]
+        ll = lse_of(*qk[0])
+        a, b = (ispa.attn_mass(q, k, ll, None, torch.zeros((2, 150), device="cuda"), cuda_cores=True) for q, k in qk)
+        assert torch.equal(a, b)
+    for hd, n_q, q_block in ((64, 2, 1), (128, 3, 1), (128, 5, 128)):
+        a, b = (ispa.block_sparse_attn(*sparse_case("bf16", 2, hd, n_q, q_block, 5, 70, 300, 64, 3, 83, p, p)[0].values(),
+                                       torch.tensor([0, 2, 4], dtype=torch.int32, device="cuda").repeat(2, -(-n_q // q_block), 1),
+                                       block=64, q_block=q_block, cuda_cores=True) for p in (0, 1))
+        assert all(torch.equal(a[w], b[w]) for w in a)
