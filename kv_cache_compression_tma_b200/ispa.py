@@ -254,16 +254,17 @@ def dual_stream_attn(q, k_sink, v_sink, k_loc, v_loc, k_hist, v_hist, *, o_loc=N
     n_q, H, hd = q.shape
     d = H * hd
     dev = q.device
-    if o_loc is None:
-        o_loc = torch.empty((n_q, d), dtype=q.dtype, device=dev)
-    if o_full is None:
-        o_full = torch.empty((n_q, d), dtype=q.dtype, device=dev)
-    if d_out is None and want_delta:
-        d_out = torch.empty((n_q, d), dtype=q.dtype, device=dev)
-    if lse_loc is None:
-        lse_loc = torch.empty((H, n_q), dtype=torch.float32, device=dev)
-    if lse_hist is None:
-        lse_hist = torch.empty((H, n_q), dtype=torch.float32, device=dev)
+    with _alloc_on(stream):
+        if o_loc is None:
+            o_loc = torch.empty((n_q, d), dtype=q.dtype, device=dev)
+        if o_full is None:
+            o_full = torch.empty((n_q, d), dtype=q.dtype, device=dev)
+        if d_out is None and want_delta:
+            d_out = torch.empty((n_q, d), dtype=q.dtype, device=dev)
+        if lse_loc is None:
+            lse_loc = torch.empty((H, n_q), dtype=torch.float32, device=dev)
+        if lse_hist is None:
+            lse_hist = torch.empty((H, n_q), dtype=torch.float32, device=dev)
     n_kv, k_ptr, v_ptr, ld_k, ld_v = [], [], [], [], []
     for k, v in ((k_sink, v_sink), (k_loc, v_loc), (k_hist, v_hist)):
         n = k.shape[0]
@@ -312,14 +313,15 @@ def absorb(G, R, S, W, lam: float, *, lam_rel: bool = False, w_transposed: bool 
     _on_current_device(G, R, S, W, dW, eps, w_new, ws)
     d = G.shape[0]
     dev = G.device
-    if dW is None:
-        dW = torch.empty((d, d), dtype=torch.float32, device=dev)
-    if eps is None:
-        eps = torch.empty((4,), dtype=torch.float64, device=dev)
-    if ws is None:
-        ws = torch.empty((absorb_workspace_size(d),), dtype=torch.uint8, device=dev)
-    if write_wnew and w_new is None:
-        w_new = torch.empty_like(W)
+    with _alloc_on(stream):
+        if dW is None:
+            dW = torch.empty((d, d), dtype=torch.float32, device=dev)
+        if eps is None:
+            eps = torch.empty((4,), dtype=torch.float64, device=dev)
+        if ws is None:
+            ws = torch.empty((absorb_workspace_size(d),), dtype=torch.uint8, device=dev)
+        if write_wnew and w_new is None:
+            w_new = torch.empty_like(W)
     flags = (ISPA_LAMBDA_REL if lam_rel else 0) | (ISPA_W_TRANSPOSED if w_transposed else 0) | \
             (ISPA_WRITE_WNEW if write_wnew else 0)
     _check(lib().ispa_absorb(_ptr(G), _ptr(R), _ptr(S), _dtype_code(W), _ptr(W), d, float(lam), flags, _ptr(dW),
@@ -339,12 +341,13 @@ def absorb_static(G, R, S, W, lam: float, *, lam_rel: bool = False, w_transposed
     _on_current_device(G, R, S, W, dW, eps, w_new)
     d = G.shape[0]
     dev = G.device
-    if dW is None:
-        dW = torch.empty((d, d), dtype=torch.float32, device=dev)
-    if eps is None:
-        eps = torch.empty((4,), dtype=torch.float64, device=dev)
-    if write_wnew and w_new is None:
-        w_new = torch.empty_like(W)
+    with _alloc_on(stream):
+        if dW is None:
+            dW = torch.empty((d, d), dtype=torch.float32, device=dev)
+        if eps is None:
+            eps = torch.empty((4,), dtype=torch.float64, device=dev)
+        if write_wnew and w_new is None:
+            w_new = torch.empty_like(W)
     flags = (ISPA_LAMBDA_REL if lam_rel else 0) | (ISPA_W_TRANSPOSED if w_transposed else 0) | \
             (ISPA_WRITE_WNEW if write_wnew else 0)
     _check(lib().ispa_absorb_static(_ptr(G), _ptr(R), _ptr(S), _dtype_code(W), _ptr(W), d, float(lam), flags,
@@ -364,7 +367,8 @@ def project(A, W, *, w_transposed: bool = False, out=None, stream=None):
     if (W.shape[1] if w_transposed else W.shape[0]) != d_in:
         raise ValueError("W does not match A's width")
     if out is None:
-        out = torch.empty((m, d_out), dtype=A.dtype, device=A.device)
+        with _alloc_on(stream):
+            out = torch.empty((m, d_out), dtype=A.dtype, device=A.device)
     flags = ISPA_W_TRANSPOSED if w_transposed else 0
     _check(lib().ispa_project(_dtype_code(A), _ptr(A), m, d_in, _row_stride(A, "A"), _ptr(W), d_out,
                               _row_stride(W, "W"), flags, _ptr(out), _row_stride(out, "out"), _stream(stream)),
@@ -379,10 +383,11 @@ def quantize_e4m3(X, *, columns: bool = False, q=None, scale=None, stream=None):
     import torch
     _on_current_device(X, q, scale)
     rows, cols = X.shape
-    if q is None:
-        q = torch.empty((cols, rows) if columns else (rows, cols), dtype=torch.uint8, device=X.device)
-    if scale is None:
-        scale = torch.empty((cols if columns else rows,), dtype=torch.float32, device=X.device)
+    with _alloc_on(stream):
+        if q is None:
+            q = torch.empty((cols, rows) if columns else (rows, cols), dtype=torch.uint8, device=X.device)
+        if scale is None:
+            scale = torch.empty((cols if columns else rows,), dtype=torch.float32, device=X.device)
     ldx = _row_stride(X, "X") if rows else cols
     ldq = _row_stride(q, "q") if q.shape[0] > 1 else q.shape[1]
     _check(lib().ispa_quantize_e4m3(_dtype_code(X), _ptr(X), rows, cols, ldx, ISPA_QUANT_COLUMNS if columns else 0,
@@ -400,7 +405,8 @@ def project_w8a8(qa, sa, qw, sw, *, out=None, stream=None):
     if qw.shape[1] != d_in:
         raise ValueError("qw does not match qa's width")
     if out is None:
-        out = torch.empty((m, d_out), dtype=torch.bfloat16, device=qa.device)
+        with _alloc_on(stream):
+            out = torch.empty((m, d_out), dtype=torch.bfloat16, device=qa.device)
     _check(lib().ispa_project_w8a8(_ptr(qa), _ptr(sa), m, d_in, _row_stride(qa, "qa"), _ptr(qw), _ptr(sw), d_out,
                                    _row_stride(qw, "qw"), _ptr(out), _row_stride(out, "out"), _stream(stream)),
            "ispa_project_w8a8")
@@ -428,10 +434,11 @@ class TempCache:
         import torch
         _on_current_device(k_new, self.k, idx, sim)
         n_new = k_new.shape[0]
-        if idx is None:
-            idx = torch.empty((self.n_heads, n_new), dtype=torch.int32, device=k_new.device)
-        if sim is None:
-            sim = torch.empty((self.n_heads, n_new), dtype=torch.float32, device=k_new.device)
+        with _alloc_on(stream):
+            if idx is None:
+                idx = torch.empty((self.n_heads, n_new), dtype=torch.int32, device=k_new.device)
+            if sim is None:
+                sim = torch.empty((self.n_heads, n_new), dtype=torch.float32, device=k_new.device)
         ld_new = _row_stride(k_new, "k_new") if n_new else self.n_heads * self.head_dim
         _check(lib().ispa_tempcache_match(self.n_heads, self.head_dim, _ptr(k_new), n_new, ld_new, _ptr(self.k),
                                           self.n_cache, self.n_heads * self.head_dim, _ptr(self.inv_norm),

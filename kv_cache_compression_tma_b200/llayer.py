@@ -45,7 +45,8 @@ def layer_forward(q, k_sink, v_sink, k_loc, v_loc, k_hist, v_hist, W, *, llayer:
     """
     n, H, hd = q.shape
     if work is None:
-        work = LayerWork(n, H, hd, q.dtype, q.device)
+        with ispa._alloc_on(stream):  # dropped on return, while the stream may still work on it
+            work = LayerWork(n, H, hd, q.dtype, q.device)
     buf = work.view(n)
     if llayer:
         k_hist = k_loc[:0]

@@ -154,3 +154,63 @@ def test_cuda_cores_flag_asks_for_fp32_arithmetic(cuda_ok):
                                        torch.tensor([0, 2, 4], dtype=torch.int32, device="cuda").repeat(2, -(-n_q // q_block), 1),
                                        block=64, q_block=q_block, cuda_cores=True) for p in (0, 1))
         assert all(torch.equal(a[w], b[w]) for w in a)
+
+
+# ------------------------------------------------------------------------------------------ streams and buffers
+def owner_of(address):
+    """The stream whose memory holds this address (the allocator's segments, blocks in use or free)."""
+    import torch
+    return [s["stream"] for s in torch.cuda.memory_snapshot() if s["address"] <= address < s["address"] + s["total_size"]]
+
+
+@pytest.mark.parametrize("llayer_,blocks", [(False, True), (False, False), (True, False)])
+def test_layer_forward_on_a_stream_works_in_its_memory(cuda_ok, monkeypatch, llayer_, blocks):
+    """Buffers that layer_forward drops on return, while a side stream still works on them, are that stream's;
+    so is the result."""
+    import torch
+    from kv_cache_compression_tma_b200 import ispa, llayer
+    t, idx = sparse_case("bf16", 2, 64, 3, 1, 5, 70, 300, 64, 3, 84)
+    W = tensor((128, 1, 128), 85, torch.bfloat16, 1 / 16.0).flatten(1)
+    seen = []
+
+    def spy(name):
+        call = getattr(ispa, name)
+
+        def wrapped(*a, **kw):
+            out = call(*a, **kw)
+            seen.extend(x.data_ptr() for x in out.values() if x is not None)
+            return out
+        monkeypatch.setattr(ispa, name, wrapped)
+
+    spy("dual_stream_attn")
+    spy("block_sparse_attn")
+    want = llayer.layer_forward(*t.values(), W, llayer=llayer_, blocks=idx if blocks else None, block=64, q_block=1)
+    seen.clear()
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    y = llayer.layer_forward(*t.values(), W, llayer=llayer_, blocks=idx if blocks else None, block=64, q_block=1, stream=side)
+    side.synchronize()
+    assert torch.equal(y, want) and len(seen) == 4
+    assert all(owner_of(a) == [side.cuda_stream] for a in seen + [y.data_ptr()])
+
+
+def test_results_of_the_other_calls_on_a_stream_come_from_its_memory(cuda_ok):
+    """The same of the calls whose results layer_forward does not reach."""
+    import torch
+    from kv_cache_compression_tma_b200 import ispa
+    d = 256
+    a = tensor((d, 1, d), 86, torch.bfloat16).flatten(1)
+    G = torch.eye(d, device="cuda") * 4
+    R, S = torch.eye(d, device="cuda"), torch.eye(d, device="cuda")
+    tc = ispa.TempCache(2, 64, 32)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    qw, sw = ispa.quantize_e4m3(a, columns=True, stream=side)
+    qa, sa = ispa.quantize_e4m3(a, stream=side)
+    out = [qw, sw, qa, sa, ispa.project_w8a8(qa, sa, qw, sw, stream=side), ispa.project(a, a, stream=side)]
+    out += [x for x in ispa.absorb(G, R, S, a, 0.1, write_wnew=True, stream=side).values()]
+    out += [x for x in ispa.absorb_static(G, R, S, a, 0.1, write_wnew=True, stream=side).values()]
+    out += tc.match(tensor((4, 2, 64), 87, torch.bfloat16), stream=side)
+    side.synchronize()
+    assert ispa.get_device_status() == ispa.ISPA_OK
+    assert all(owner_of(x.data_ptr()) == [side.cuda_stream] for x in out)
