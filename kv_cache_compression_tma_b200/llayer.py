@@ -26,8 +26,10 @@ class LayerWork:
         self.lse_hist = torch.empty_like(self.lse_loc)
 
     def view(self, n: int) -> Dict[str, object]:
-        return {"o_loc": self.o_loc[:n], "o_full": self.o_full[:n], "lse_loc": self.lse_loc[:, :n],
-                "lse_hist": self.lse_hist[:, :n]}
+        """The buffers of a chunk of n rows; the lse arrays are dense [H, n], as the calls write them."""
+        H = self.lse_loc.shape[0]
+        lse = [x.view(-1)[:H * n].view(H, n) for x in (self.lse_loc, self.lse_hist)]
+        return {"o_loc": self.o_loc[:n], "o_full": self.o_full[:n], "lse_loc": lse[0], "lse_hist": lse[1]}
 
 
 def layer_forward(q, k_sink, v_sink, k_loc, v_loc, k_hist, v_hist, W, *, llayer: bool, w_transposed: bool = False,
@@ -52,9 +54,8 @@ def layer_forward(q, k_sink, v_sink, k_loc, v_loc, k_hist, v_hist, W, *, llayer:
         k_hist = k_loc[:0]
         v_hist = v_loc[:0]
     if blocks is not None and not llayer:
-        # the row-shaped lse buffers of a smaller chunk are not contiguous views: let the call allocate them
         ispa.block_sparse_attn(q, k_sink, v_sink, k_loc, v_loc, k_hist, v_hist, blocks, block=block, q_block=q_block,
-                               o_loc=buf["o_loc"], o_full=buf["o_full"], want_delta=False, stream=stream)
+                               want_delta=False, stream=stream, **buf)
     else:
         ispa.dual_stream_attn(q, k_sink, v_sink, k_loc, v_loc, k_hist, v_hist, want_delta=False, stream=stream, **buf)
     a = buf["o_loc"] if llayer else buf["o_full"]

@@ -214,3 +214,23 @@ def test_results_of_the_other_calls_on_a_stream_come_from_its_memory(cuda_ok):
     side.synchronize()
     assert ispa.get_device_status() == ispa.ISPA_OK
     assert all(owner_of(x.data_ptr()) == [side.cuda_stream] for x in out)
+
+
+@pytest.mark.parametrize("blocks", [False, True])
+def test_layer_work_holds_the_log_sum_exps_of_a_smaller_chunk(cuda_ok, blocks):
+    """A LayerWork made for more rows: its views are arrays as the calls write them, and layer_forward
+    allocates nothing but its result."""
+    import torch
+    from kv_cache_compression_tma_b200 import ispa, llayer
+    t, idx = sparse_case("bf16", 4, 64, 5, 1, 5, 70, 300, 64, 3, 88)
+    W = tensor((256, 1, 256), 89, torch.bfloat16, 1 / 16.0).flatten(1)
+    work = llayer.LayerWork(9, 4, 64, torch.bfloat16)
+    y = torch.empty((5, 256), dtype=torch.bfloat16, device="cuda")
+    call = lambda: llayer.layer_forward(*t.values(), W, llayer=False, work=work, out=y, blocks=idx if blocks else None, block=64, q_block=1)
+    call()
+    n0 = torch.cuda.memory_stats()["allocation.all.allocated"]
+    call()
+    assert torch.cuda.memory_stats()["allocation.all.allocated"] == n0
+    want = ispa.block_sparse_attn(*t.values(), idx, block=64) if blocks else ispa.dual_stream_attn(*t.values())
+    view = work.view(5)
+    assert all(torch.equal(view[w], want[w]) for w in ("o_loc", "o_full", "lse_loc", "lse_hist"))
