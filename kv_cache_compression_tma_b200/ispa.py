@@ -556,7 +556,8 @@ class MassCache:
         self.seen = 0  # tokens inserted so far: the next token's position
 
     def segment(self):
-        """(k, v) views of the held entries, for dual_stream_attn's history segment."""
+        """(k, v) views of the held entries, for dual_stream_attn's history segment.  insert replaces entries in
+        place, so what is kept about these keys (a BlockIndex's means) holds until the next insert only."""
         return self.k[:self.n], self.v[:self.n]
 
     def accumulate(self, q, lse_loc, lse_hist=None, *, decay: float = 1.0, softmax_scale: float = 0.0, stream=None):
@@ -622,10 +623,14 @@ class BlockIndex:
 
     def extend(self, k, stream=None):
         """Pool the blocks of the history k [n, H, hd] that its tokens since the last call touch.  The history
-        only grows at its end; reset() starts another."""
-        if k.shape[0] < self.n:
+        only grows at its end; reset() starts another.  A MassCache's entries change in place, so its
+        segment's views are no such history: pass the MassCache itself, whose blocks are all pooled anew."""
+        first = self.n // self.block
+        if isinstance(k, MassCache):
+            k, first = k.k[:k.n], 0
+        elif k.shape[0] < self.n:
             raise ValueError(f"the history had {self.n} tokens and now has {k.shape[0]}: reset() first")
-        block_means(k, self.means, self.block, first=self.n // self.block, stream=stream)
+        block_means(k, self.means, self.block, first=first, stream=stream)
         self.n = k.shape[0]
 
     def reset(self):

@@ -234,3 +234,20 @@ def test_layer_work_holds_the_log_sum_exps_of_a_smaller_chunk(cuda_ok, blocks):
     want = ispa.block_sparse_attn(*t.values(), idx, block=64) if blocks else ispa.dual_stream_attn(*t.values())
     view = work.view(5)
     assert all(torch.equal(view[w], want[w]) for w in ("o_loc", "o_full", "lse_loc", "lse_hist"))
+
+
+def test_block_index_over_a_cache_whose_slots_change(cuda_ok):
+    """Insertion replaces entries in place: a BlockIndex that is given the MassCache itself pools what it holds
+    now, while the cache fills, when it first evicts and when its length no longer changes."""
+    import torch
+    from kv_cache_compression_tma_b200 import ispa
+    H, hd, cap = 2, 64, 200
+    mc, bi = ispa.MassCache(H, hd, cap), ispa.BlockIndex(H, hd, cap, block=64)
+    for step in range(4):
+        new = [tensor((90, H, hd), 90 + 2 * step + i, torch.bfloat16) for i in range(2)]
+        mc.insert(*new, torch.rand((H, 90), device="cuda"))
+        bi.extend(mc)
+        assert mc.n == min(cap, 90 * (step + 1))
+        nb = -(-mc.n // 64)
+        assert np.array_equal(bi.means[:nb].cpu().numpy(), orc.block_means(host(mc.k[:mc.n]), 64).astype(np.float32))
+        assert bi.select(new[0][:1], 2).max().item() < nb
