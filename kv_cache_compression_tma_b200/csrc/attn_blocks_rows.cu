@@ -7,8 +7,8 @@
 // an online-softmax state (max, sum, accumulator) per branch; the states are joined by log-sum-exp in a
 // fixed order: lanes by shuffles, warps in shared memory, CTAs through distributed shared memory.
 //   bf16, head_dim 64 or 128, 16-byte aligned rows: units of 16 keys, both products by mma.m16n8k16.
-//   S = K q^T has the query as one of eight columns; O^T = V^T p^T has the weights as two, p rounded to
-//   bf16 and what the rounding left (so p keeps 16 bits, at no further instruction).  Each warp copies
+//   S = K q^T has the query as one of eight columns; O^T = V^T p^T has the weights as three, p rounded to
+//   bf16 and twice what the rounding left (so p keeps its 24 bits, at no further product).  Each warp copies
 //   its units ahead (cp.async) into its own ring of kStages units in shared memory.  (By multiply-adds
 //   and shuffles a unit took over 400 instructions, and their latency, not memory, set the pace.)
 //   Other cases (and bf16 with ISPA_ATTN_CUDA_CORES): a key row spans kLanes lanes (16 bytes each), units of 8 warp-wide loads, dot products
@@ -192,14 +192,16 @@ __global__ void __launch_bounds__(Kind<T, HD, kAligned, kMma>::kThreads, Kind<T,
     const float p0 = fast_exp2(s0 - ref), p1 = fast_exp2(s1 - ref);
     lb += p0 + p1;  // of the lanes with mc == 0
     // weights as the second operand: column mg, keys 2 mc + {0, 1} and 8 more; column 0 the rounded
-    // weights, column 1 what the rounding left, the others zero
+    // weights, columns 1 and 2 what the rounding before left, the others zero
     uint32_t w[2];
 #pragma unroll
     for (int x = 0; x < 2; ++x) {
       const float a0 = __shfl_sync(0xffffffffu, x ? p1 : p0, 8 * mc), a1 = __shfl_sync(0xffffffffu, x ? p1 : p0, 8 * mc + 4);
       const uint32_t hi = pack_bf16x2(a0, a1);
-      const uint32_t lo = pack_bf16x2(a0 - __uint_as_float(hi << 16), a1 - __uint_as_float(hi & 0xFFFF0000u));
-      w[x] = mg == 0 ? hi : (mg == 1 ? lo : 0u);
+      const float r0 = a0 - __uint_as_float(hi << 16), r1 = a1 - __uint_as_float(hi & 0xFFFF0000u);
+      const uint32_t mid = pack_bf16x2(r0, r1);
+      const uint32_t lo = pack_bf16x2(r0 - __uint_as_float(mid << 16), r1 - __uint_as_float(mid & 0xFFFF0000u));
+      w[x] = mg == 0 ? hi : (mg == 1 ? mid : (mg == 2 ? lo : 0u));
     }
     // first operand: rows 16 t + {0..15} of V^T, the four 8 x 8 parts by one transposing load
     const int r = ((lane >> 4) & 1) * 8 + (lane & 7);
@@ -318,13 +320,14 @@ __global__ void __launch_bounds__(Kind<T, HD, kAligned, kMma>::kThreads, Kind<T,
         sm[br][warp] = from ? m[1] : m[0];
         sl[br][warp] = lw;
       }
-      if (mc == 0) {
 #pragma unroll
-        for (int t = 0; t < HD / 16; ++t) {
-          const float* o = from ? dacc[1][kMma ? t : 0] : dacc[0][kMma ? t : 0];
+      for (int t = 0; t < HD / 16; ++t) {
+        const float* o = from ? dacc[1][kMma ? t : 0] : dacc[0][kMma ? t : 0];
+        const float lo0 = __shfl_down_sync(0xffffffffu, o[0], 1), lo2 = __shfl_down_sync(0xffffffffu, o[2], 1);  // column 2
+        if (mc == 0) {
           // an infinite value times a remainder of zero or of the other sign is no part of the sum
-          sacc[br][warp][16 * t + mg] = o[0] + (isfinite(o[0]) ? o[1] : 0.f);
-          sacc[br][warp][16 * t + 8 + mg] = o[2] + (isfinite(o[2]) ? o[3] : 0.f);
+          sacc[br][warp][16 * t + mg] = o[0] + (isfinite(o[0]) ? o[1] + lo0 : 0.f);
+          sacc[br][warp][16 * t + 8 + mg] = o[2] + (isfinite(o[2]) ? o[3] + lo2 : 0.f);
         }
       }
     }

@@ -251,3 +251,29 @@ def test_block_index_over_a_cache_whose_slots_change(cuda_ok):
         nb = -(-mc.n // 64)
         assert np.array_equal(bi.means[:nb].cpu().numpy(), orc.block_means(host(mc.k[:mc.n]), 64).astype(np.float32))
         assert bi.select(new[0][:1], 2).max().item() < nb
+
+
+@pytest.mark.parametrize("hd", [64, 128])
+def test_sparse_rows_weigh_values_in_fp32(cuda_ok, hd):
+    """Three keys of weights 1, x and 1 with values -b1, 1 and -b2, where b1 + b2 are the first 16 bits of x: what
+    is left, (x - b1 - b2) / (2 + x), is below 2.6e-6 and lost to weights of 16 bits.  The scores are one product each,
+    |y| <= 2.2 in base 2; x is good to 2^-22 (the exponential), 4 2^-24 |y| ln 2 (scale, difference) and 2^-22 (two
+    sums in the tensor core), in all 9e-7 of x <= 1, so 3e-7 of the quotient."""
+    import torch
+    from kv_cache_compression_tma_b200 import ispa
+    H, n_q = 24, 3
+    q, k, v = (torch.zeros((n, H, hd), dtype=torch.bfloat16, device="cuda") for n in (n_q, 3, 3))
+    q[:, :, 0] = torch.tensor([1.0, 0.75, 0.5], device="cuda")[:, None]
+    k[1, :, 0] = -(0.5 + torch.arange(H, device="cuda") * 0.46875) * (hd / 64) ** 0.5
+    x = torch.exp(q.double()[:, :, 0] * k.double()[1, :, 0] / hd ** 0.5)  # [n_q, H]
+    b1 = x.to(torch.bfloat16)
+    b2 = (x - b1.double()).to(torch.bfloat16)
+    v[1] = 1.0
+    for i in range(n_q):  # a value column per query
+        v[0, :, i], v[2, :, i] = -b1[i], -b2[i]
+    want = (x - b1.double() - b2.double()) / (2.0 + x)
+    none = torch.zeros((H, n_q, 0), dtype=torch.int32, device="cuda")
+    out = ispa.block_sparse_attn(q, k[:0], v[:0], k, v, k[:0], v[:0], none, block=64)
+    got = torch.stack([out["o_loc"].view(n_q, H, hd)[i, :, i] for i in range(n_q)]).double()
+    assert want.abs().max().item() > 1e-6
+    assert (got - want).abs().max().item() <= 3e-7 + 2.0 ** -8 * 2.6e-6
