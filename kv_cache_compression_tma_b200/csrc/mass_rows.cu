@@ -131,7 +131,7 @@ __global__ void __launch_bounds__(kThreads) mass_rows_kernel(const MassLaunch a)
   using R = Row<T, HD>;
   constexpr int kWarpKeys = R::kPerWarp * kRows;
   constexpr int kKeys = kSplit ? kWarpKeys : kWarps * kWarpKeys;  // keys per step of a CTA
-  __shared__ float sq[kQTile][HD];
+  __shared__ __align__(16) float sq[kQTile][HD];  // read four at a time
   __shared__ float sl[kQTile], sl_lo[kQTile];  // L and what its rounding left
   __shared__ float part[kSplit ? kWarps : 1][kWarpKeys];
   const int head = static_cast<int>(blockIdx.x % a.n_heads);  // heads first: CTAs that run together share rows
