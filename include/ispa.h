@@ -328,9 +328,12 @@ ISPA_API ispa_status ispa_tempcache_merge(int32_t n_heads, int32_t head_dim, voi
  *   the attention took it for this segment (finite values in [-64, 16], -inf excludes a key, whose
  *   weight is then 0 whatever its key holds); any alignment.  softmax_scale 0 selects 1/sqrt(head_dim).
  * ISPA_BF16: head_dim 64 or 128, else ISPA_ERR_UNSUPPORTED unless flags has ISPA_ATTN_CUDA_CORES, which
- * admits 16 and 32 too.  ISPA_F32: head_dim 16, 32, 64 or 128, on CUDA cores.  Any alignment; bf16
- * keys and queries at 16-byte aligned addresses with strides that are multiples of 8 run on the tensor
- * cores.  Deterministic.  n_k == 0 is a no-op; n_q == 0 only decays.
+ * admits 16 and 32 too and asks for fp32 multiply-adds.  ISPA_F32: head_dim 16, 32, 64 or 128, on CUDA
+ * cores.  Any alignment; bf16 keys and queries at 16-byte aligned addresses with strides that are multiples
+ * of 8 run on the tensor cores, products and sums in fp32.  Beside the rounding of logits, L is held in 64
+ * bits for up to 32 queries and on CUDA cores; with more on the tensor cores it is one fp32 number (2^-24 of
+ * |L| in every weight of a query, whose sign changes from query to query) and a quarter of the exponentials
+ * are good to 2.7e-6 (mean 4e-8), the others to 2^-22.  Deterministic.  n_k == 0 is a no-op; n_q == 0 only decays.
  */
 ISPA_API ispa_status ispa_attn_mass(int32_t dtype, int32_t n_heads, int32_t head_dim, const void* q, int64_t n_q,
                                     int64_t ld_q, const void* k, int64_t n_k, int64_t ld_k, const float* lse_loc,
@@ -401,7 +404,8 @@ ISPA_API ispa_status ispa_block_select(int32_t dtype, int32_t n_heads, int32_t h
  *   listed twice counts twice.  A row without any history key gets lse_hist = -inf, O_full = O_loc and
  *   D = 0.  n_sel == 0 (idx unused) is attention over sink and local alone.
  * o_loc, o_full and d_out must not overlap (the tensor-core kernel keeps part of O_loc in o_full meanwhile).
- * Every entry of idx is read on the device when the kernel runs.  ISPA_BF16 with q_block a multiple of
+ * Every entry of idx is read on the device when the kernel runs.  Statistics and sums are fp32; the tensor-core
+ * kernel rounds P to bf16 for the P V product, the row kernel does not.  ISPA_BF16 with q_block a multiple of
  * 128 runs on the tensor cores (block 64 or 128, n_sel <= 4096, head_dim 64 or 128 and the alignment rules
  * of ispa_dual_stream_attn, else ISPA_ERR_UNSUPPORTED; calls of few rows take the row kernel there too),
  * ISPA_BF16 with q_block 1 (each query its own picks: the single-token form) on the row kernel, at any

@@ -1,6 +1,6 @@
 // attn_blocks_rows.cu -- dual-stream attention over sink, local and selected history blocks, one
-// query row and head per cluster (CUDA cores, fp32 arithmetic): the single-token form (bf16, each
-// query with its own picks) and the kernel of every fp32 call.
+// query row and head per cluster, statistics and sums in fp32: the single-token form (bf16, each query with
+// its own picks), the form of few rows, and the kernel of every fp32 call.
 //
 // The row's keys are cut into units inside one segment or one picked block, and the units go round-robin
 // to the warps of the cluster, so a single token's keys are read by many SMs at once.  Each warp keeps

@@ -47,9 +47,12 @@ void count(int n) { g_launches.fetch_add(static_cast<uint64_t>(n)); }
 
 bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
 
-// Up to this many (query, head) rows, block-sparse attention of whole row groups takes the row kernel, one
-// CTA per row and SM: over 7216 keys 27 us for 40 rows, 49 for 80 to 144, against 55 to 57 on the tensor
-// cores; at 160 rows a second wave makes it 96 (each row reads its keys for itself).
+// Up to this many (query, head) rows, block-sparse attention of whole row groups takes the row kernel: one
+// wave of clusters, a CTA per SM.  Against the tensor cores, us at 256 / 2048 / 8192 / 131072 keys per row:
+// 8 rows of one head 8 / 9 / 15 / 114 (12 / 23 / 59 / 789); 40 of 40 heads 9 / 13 / 33 / 379 (12 / 24 / 65 /
+// 838); 64 of one 9 / 15 / 35 / 428 (14 / 25 / 61 / 792).  From 75 rows on a row has one CTA, and from 16384
+// keys on the two are level: 128 of one head 9 / 21 / 61 / 848 (17 / 28 / 65 / 806), 144 of twelve 10 / 21 /
+// 62 / 850 (13 / 24 / 61 / 835).  A second wave (160 rows, 7216 keys) takes 96 against 57.
 constexpr int64_t kBlockRowsMax = 148;
 
 // Heads of the bounded-history calls: one grid dimension of 65535 covers a row's 256-byte pieces at any

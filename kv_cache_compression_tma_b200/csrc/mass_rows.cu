@@ -1,8 +1,10 @@
-// mass_rows.cu -- accumulated attention weight per cached key on CUDA cores (fp32 arithmetic).
+// mass_rows.cu -- accumulated attention weight per cached key for few bf16 queries (mma.sync) and on CUDA
+// cores (fp32 multiply-adds).
 //
 //   mass_out[h, j] = decay * mass[h, j] + sum_i exp(scale q_i.k_j + b_j - L_i),
 //   L_i = log(exp(lse_loc_i) + exp(lse_hist_i)),
-// for few queries (single-token steps, bf16) and for every fp32 call.  K is read once whatever n_q is.
+// for few queries (single-token steps, bf16) and for every fp32, unaligned or ISPA_ATTN_CUDA_CORES call.  K is
+// read once whatever n_q is.
 //
 // Up to 32 bf16 queries: a warp takes 16 keys at a time, their rows go from memory straight into the
 // fragments of mma.m16n8k16 (8 query columns cost the same as one), and the next 16 keys are loaded

@@ -233,7 +233,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     // ------------------------------------------------------------------ sums
     const int quarter = warp & 3;  // TMEM lane quarter this warp may access
     const int wg = (warp - kFirstEpiWarp) >> 2;
-    const int sel = wg & 1, half = wg >> 1;  // which accumulator, which 128 of its columns
+    const int sel = wg & 1, half = wg >> 1;  // which accumulator, which 64 of its columns
     const int row = quarter * 32 + lane;     // key within the tile == TMEM lane
     const int tid = wg * 128 + row;
     const uint32_t lane_addr = static_cast<uint32_t>(quarter * 32) << 16;
