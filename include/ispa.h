@@ -403,7 +403,8 @@ ISPA_API ispa_status ispa_block_select(int32_t dtype, int32_t n_heads, int32_t h
  *   idx[h, i, :], in any order; an entry outside 0 .. ceil(n_hist / block) - 1 names no block, a block
  *   listed twice counts twice.  A row without any history key gets lse_hist = -inf, O_full = O_loc and
  *   D = 0.  n_sel == 0 (idx unused) is attention over sink and local alone.
- * o_loc, o_full and d_out must not overlap (the tensor-core kernel keeps part of O_loc in o_full meanwhile).
+ * o_loc, o_full and d_out must not overlap (the tensor-core kernel keeps part of O_loc in o_full meanwhile);
+ * two that start at one address are refused.
  * Every entry of idx is read on the device when the kernel runs.  Statistics and sums are fp32; the tensor-core
  * kernel rounds P to bf16 for the P V product, the row kernel does not.  ISPA_BF16 with q_block a multiple of
  * 128 runs on the tensor cores (block 64 or 128, n_sel <= 4096, head_dim 64 or 128 and the alignment rules

@@ -546,6 +546,7 @@ ispa_status ispa_block_sparse_attn(const ispa_attn_args* a, const int32_t* idx, 
   if (groups && !attn_blocks_tc_supported(L, B)) return ISPA_ERR_UNSUPPORTED;
   const bool rows = !groups || a->n_q * a->n_heads <= kBlockRowsMax;
   if (a->n_q == 0) return ISPA_OK;
+  if (a->o_loc == a->o_full || a->d_out == a->o_loc || a->d_out == a->o_full) return ISPA_ERR_INVALID_ARG;
   L.status = status_ptr();
   if (!L.status) return ISPA_ERR_CUDA;
   cudaStream_t st = static_cast<cudaStream_t>(stream);

@@ -238,3 +238,11 @@ def test_sizes_past_the_abis_integers_are_refused(monkeypatch):
         with pytest.raises(ValueError):
             cache.insert(k, k, **kw)
     assert cache.seen == 2 ** 31 and cache.n == 0
+
+
+def test_block_sparse_outputs_must_differ(ispa):
+    """Two outputs in one array: the tensor-core kernel keeps part of one in the other's place meanwhile."""
+    f = ispa.lib().ispa_block_sparse_attn
+    for same in ({}, dict(o_full=2 * P, d_out=P), dict(o_full=2 * P, d_out=2 * P)):
+        for q_block in (1, 128):
+            assert f(ctypes.byref(attn_args(ispa, **same)), P, 2, 64, q_block, None) == 1
