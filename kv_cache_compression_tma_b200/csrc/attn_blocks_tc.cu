@@ -101,6 +101,51 @@ __device__ __forceinline__ void store_tile_2d(const CUtensorMap* map, const void
                : "memory");
 }
 
+__device__ __forceinline__ uint4 pack8(const float* v) {
+  return make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7]));
+}
+
+// O_loc, kCols columns of a thread's row from TMEM: rounded, to its place; with a history, the lower 16 bits of the
+// fp32 value wait in O_full's.  Read as a signed number they are what the rounding left, so adding them below the
+// rounded value's bits gives the fp32 value again; only a value halfway between two bf16 ones (read as -32768
+// either way) cannot be told from its neighbour and moves to the even one's side first, by one unit of fp32.
+// Not inlined: the softmax loop around its call keeps its registers (410 -> 405 us on the case above).
+template <int kCols>
+__device__ __noinline__ void set_aside(uint32_t src, float inv_l, __nv_bfloat16* o_loc, __nv_bfloat16* o_full,
+                                       bool has_hist, bool live) {
+#pragma unroll 1
+  for (int c = 0; c < kCols / 16; ++c) {
+    uint32_t o0[16];
+    float o[16];
+    tmem_ld16(src + c * 16, o0);
+    tmem_wait_ld();
+#pragma unroll
+    for (int j = 0; j < 16; ++j) o[j] = __uint_as_float(o0[j]) * inv_l;
+    if (live) {
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        if (has_hist) {
+          uint32_t lo[4];
+#pragma unroll
+          for (int j = 0; j < 8; j += 2) {
+            uint32_t b[2];
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+              b[x] = __float_as_uint(o[8 * i + j + x]);
+              if ((b[x] & 0xFFFFu) == 0x8000u) b[x] += (b[x] & 0x10000u) ? 1u : 0xFFFFFFFFu;
+              o[8 * i + j + x] = __uint_as_float(b[x]);
+            }
+            lo[j / 2] = __byte_perm(b[0], b[1], 0x5410);
+          }
+          *reinterpret_cast<uint4*>(o_full + c * 16 + 8 * i) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+        }
+        *reinterpret_cast<uint4*>(o_loc + c * 16 + 8 * i) = pack8(o + 8 * i);
+      }
+    }
+    __syncwarp();  // the next columns' load takes the whole warp
+  }
+}
+
 template <int HD>
 __global__ void __launch_bounds__(kThreads, 1) attn_blocks_tc_kernel(const __grid_constant__ Maps maps, const Params p) {
   using C = Cfg<HD>;
@@ -321,40 +366,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_blocks_tc_kernel(const __gri
     };
     const bool live_row = q0 + row < p.n_q;
     const int64_t o_at = static_cast<int64_t>(q0 + row) * p.ld_o + head * HD + o_col;
-    auto pack8 = [](const float* v) {
-      return make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7]));
-    };
-    // O_loc rounded goes to its place; with a history, the lower 16 bits of the fp32 value wait in O_full's.  Read as
-    // a signed number they are what the rounding left, so adding them below the rounded value's bits gives the
-    // fp32 value again; only a value halfway between two bf16 ones (read as -32768 either way) cannot be told
-    // from its neighbour and moves to the even one's side first, by one unit of fp32.
     auto store_local = [&]() {
-      const float inv_l = 1.f / l_row;
-#pragma unroll 1
-      for (int c = 0; c < kOCols / 16; ++c) {
-        float o[16];
-        output(c, inv_l, o);
-        if (!live_row) continue;
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          if (has_hist) {
-            uint32_t lo[4];
-#pragma unroll
-            for (int j = 0; j < 8; j += 2) {
-              uint32_t b[2];
-#pragma unroll
-              for (int x = 0; x < 2; ++x) {
-                b[x] = __float_as_uint(o[8 * i + j + x]);
-                if ((b[x] & 0xFFFFu) == 0x8000u) b[x] += (b[x] & 0x10000u) ? 1u : 0xFFFFFFFFu;
-                o[8 * i + j + x] = __uint_as_float(b[x]);
-              }
-              lo[j / 2] = __byte_perm(b[0], b[1], 0x5410);
-            }
-            *reinterpret_cast<uint4*>(p.o_full + o_at + c * 16 + 8 * i) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
-          }
-          *reinterpret_cast<uint4*>(p.o_loc + o_at + c * 16 + 8 * i) = pack8(o + 8 * i);
-        }
-      }
+      set_aside<kOCols>(tmem + lane_addr + kTmemO + o_col, 1.f / l_row, p.o_loc + o_at, p.o_full + o_at, has_hist, live_row);
     };
     // the eight values of O_loc set aside at `at`
     auto load_local = [&](int64_t at, float* v) {
