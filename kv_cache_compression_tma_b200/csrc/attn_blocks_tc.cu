@@ -20,12 +20,13 @@
 //
 // Bound: the loop of three tiles (softmax of one, P V and the S that waits for its buffer) at about 1430
 // clocks per tile (1024 of MMA), and power.  12 heads x 4680 queries over 6240 local keys and 64 blocks of
-// 128 (415 GFLOP, 0.254 ms at the measured bf16 peak): 0.39 ms alone, tensor pipe 59 % busy, 0.46 ms back
-// to back at 995 W.  Measured beside it: two threads per row and one group on two S buffers, a second
-// accumulator (2090 clocks, 0.49 ms); two groups with accumulators of their own on two S buffers (the
-// same); two threads per row here (0.467 against 0.452); S read a second time instead of held in
-// registers (0.50); the two products issued by two warps (their operands alternate: 10 % slower);
-// three V stages and polynomial exponentials (nothing, and slower).
+// 128 (415 GFLOP, 0.254 ms at the measured bf16 peak): 0.40 ms alone, tensor pipe 62 % busy, 0.47 ms back
+// to back at 990 W.  The softmax warps are capped at 168 registers (eleven warps are allocated as twelve)
+// and spill 68 bytes, about 7 loads from L1 per warp and tile.  Measured beside it: two threads per row and
+// one group on two S buffers, a second accumulator (2090 clocks, 0.49 ms); two groups with accumulators of
+// their own on two S buffers (the same); two threads per row here (0.467 against 0.452); S read a second
+// time instead of held in registers (0.50); the two products issued by two warps (their operands
+// alternate: 10 % slower); three V stages and polynomial exponentials (nothing, and slower).
 //
 // Warp roles (352 threads): warp 0 Q and the K ring, warp 2 the V ring, warp 1 TMEM and the MMAs, warps
 // 3..10 softmax and epilogue.  Commits: s_full[t%3] (also frees K_t), o_done[t%2] (also frees V_t).

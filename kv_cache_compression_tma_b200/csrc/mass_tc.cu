@@ -15,10 +15,11 @@
 // it computes.  Sixteen warps, because the work per element is a chain (scale, exponential, add) whose
 // latency eight do not cover.
 //
-// Bound: exponentials and products together, under the power cap.  12 heads x 4680 queries x 14040 keys:
-// 0.204 ms in a short burst (202 GFLOP, 0.124 ms at the measured bf16 peak; 0.171 ms if the
-// special-function unit did every exponential at 1965 MHz), 0.237 ms back to back at 995 W and 1.6 GHz,
-// with 71 % of that unit, 48 % of the multiply-add pipes and 47 % of the tensor pipe busy.  Measured
+// Bound: the hand-over of accumulators between the MMAs and the drain warps, then the exponentials, then the power
+// cap.  12 heads x 4680 queries x 14040 keys: 0.205 ms in a short burst (202 GFLOP, 0.124 ms at the
+// measured bf16 peak; 0.171 ms if the special-function unit did every exponential at 1965 MHz), 0.240 ms
+// back to back at 990 W and 1.65 GHz, with 72 % of that unit, 66 % of the issue slots and 47 % of the
+// tensor pipe busy.  Measured
 // beside it: 0.246 ms with 8 warps and 0.234 with 16 while a lone lane issued the MMAs (the warp-uniform
 // form has fewer instructions to squeeze in between the sixteen busy warps; 0.243 -> 0.226 on one
 // variant), 0.226 without the polynomial exponential, 0.205 with products 192 or 256 queries wide on two
@@ -270,7 +271,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       float total = 0.f;
       for (int c0 = 0; c0 < p.n_q; c0 += kChunk) {
         const int c1 = min(p.n_q, c0 + kChunk);
-        if (head != staged_head || p.n_q > kChunk) {  // -L of the chunk's queries; padding rows get weight 0
+        // -L of the chunk's queries; padding rows get weight 0.  One fp32 number each: its rounding, 2^-24 of |L|, goes
+        // one way in one query and the other in the next, and a second number would take a fused add per weight.
+        if (head != staged_head || p.n_q > kChunk) {
           asm volatile("bar.sync 1, %0;" ::"n"(kEpiThreads) : "memory");
           for (int i = tid; i < (c1 - c0 + kQTile - 1) / kQTile * kQTile; i += kEpiThreads) {
             const int64_t o = static_cast<int64_t>(head) * p.n_q + c0 + i;
